@@ -111,6 +111,62 @@ typedef struct {
 MOE_API moe_status_t moe_route_topk(const float* logits, int32_t T, int32_t E, int32_t K,
                             int32_t* topk_idx, float* topk_w, hipStream_t stream);
 
+/* The score of an expert in moe_route_scored, from the token's logits l. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* exp(l_e) / sum over the token's experts exp(l_i) */
+  MOE_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
+} moe_score_t;
+
+/* How moe_route_scored picks experts and weighs them. */
+typedef struct {
+  int32_t T, E, K;
+  moe_score_t score;
+  int32_t groups;      /* expert groups of E / groups neighbouring experts; 1: no groups */
+  int32_t topk_groups; /* groups that stay per token; = groups: all of them */
+  int32_t group_top;   /* 1 or 2: a group's score is the sum of its so many largest choices */
+  int32_t renorm;      /* 1: weights divided by their sum over the picks; 0: the scores */
+  float scale;         /* factor on every weight */
+} moe_route_desc_t;
+
+/* Routing by scores ("Mixture of Kittens", Step 1, the router picks the top-k experts and weighs them;
+ * "Distributed expert parallelism", node-limited routing: a token's experts come from a few
+ * groups). For each token:
+ *     s_e   its experts' scores (d->score),
+ *     c_e = s_e + bias_e, the choice; without a bias c_e = l_e (the same order as s_e),
+ *     the topk_groups groups with the largest group scores stay: the sum of the group_top
+ *     largest c of the group (without a bias and with group_top = 2: of the largest s),
+ *     topk_idx = the K experts of those groups with the largest c, largest first,
+ *     topk_w_k = scale * s_k, divided by the sum of the picks' s when renorm.
+ * The bias balances the load; it takes part in the choice only, not in the weights.
+ *  - Choices and group scores are compared as if in binary64; equal ones go to the lower id.
+ *  - A logit that is NaN, -inf or the lowest value of its type masks the expert: score 0, never
+ *    picked, no part in group scores. So does a bias of NaN or -inf, for the choice only. +inf
+ *    counts as the largest fp32 value. Where fewer than K experts remain, the other picks have
+ *    topk_idx = -1 and weight 0: copies that moe_permute drops (and that MOE_VALIDATE=1 reports).
+ *  - A group scored with two choices but holding one unmasked expert has that one's choice.
+ *  logits [T, E] of logits_dtype (F32 or BF16); bias [E] fp32 or NULL; topk_idx [T, K] int32 and
+ *  topk_w [T, K] fp32 out. One kernel launch, deterministic; scores and weights in fp32.
+ * Limits: 1 <= K <= 32, E <= 1024, groups <= 64 (MOE_EUNSUPPORTED beyond); E % groups == 0,
+ * 1 <= topk_groups <= groups, group_top <= E / groups and K <= topk_groups * E / groups, a
+ * finite scale (MOE_EINVAL otherwise). */
+MOE_API moe_status_t moe_route_scored(const moe_route_desc_t* d, const void* logits,
+                                      moe_dtype_t logits_dtype, const float* bias, int32_t* topk_idx,
+                                      float* topk_w, hipStream_t stream);
+
+/* The gradient of the logits of moe_route_scored for given picks (the choice has none): with
+ * d_k = d_topk_w[t, k] and r_k the pick's share of the picks' scores,
+ *     renorm:   d_logits_e = scale r_k (d_k - sum_j d_j r_j)  [times 1 - s_k for sigmoid scores]
+ *     sigmoid:  d_logits_e = scale d_k s_k (1 - s_k)
+ *     softmax:  d_logits_e = scale s_e ([e picked] d_k - sum_j d_j s_j)   for every expert
+ * and 0 for experts that are not picked in the first two forms. Ids outside [0, E) and masked
+ * experts take no part; an expert that appears twice gets the sum of its picks' gradients.
+ *  d as in the forward call (the group fields are checked but not used); logits, topk_idx as
+ *  there; d_topk_w [T, K] fp32 (moe_layer_backward writes it); d_logits [T, E] of logits_dtype
+ *  out, written in full. One kernel launch, deterministic, fp32 throughout. */
+MOE_API moe_status_t moe_route_scored_backward(const moe_route_desc_t* d, const void* logits,
+                                               moe_dtype_t logits_dtype, const int32_t* topk_idx,
+                                               const float* d_topk_w, void* d_logits, hipStream_t stream);
+
 /* Scratch bytes moe_permute needs for (T, E, K). */
 MOE_API size_t moe_permute_workspace_bytes(int32_t T, int32_t E, int32_t K);
 
@@ -222,6 +278,37 @@ MOE_API moe_status_t moe_pack_mxfp4_pairs(const uint8_t* w, uint8_t* w_paired, i
  *  q [R, C] codes out (8-byte aligned); sf [R, C/128] fp32 out (the x_sf layout). */
 MOE_API moe_status_t moe_quantize_fp8(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t C,
                               uint8_t* q, float* sf, hipStream_t stream);
+
+/* Activations to MXFP4 ("Mixture of Kittens", Step 8): for each row r and block b of 32 columns
+ * X = 2^(floor(log2 max|x|) - 2), at least 2^-127 (also for an all-zero block), and
+ * q = e2m1 round-to-nearest-even(x / X), saturating at 6; an exact zero gives code 0. A block
+ * with an infinity or a NaN gets scale byte 255 (NaN) and zero codes.
+ *  x [R, C] of x_dtype (BF16 or F32), 16-byte aligned, C % 32 == 0;
+ *  q [R, C/2] out, 4-byte aligned: byte j of a row holds column 2j in its low nibble;
+ *  sf [R, C/32] out: X = 2^(byte - 127). One kernel launch, HBM-bound. */
+MOE_API moe_status_t moe_quantize_mxfp4(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t C,
+                                        uint8_t* q, uint8_t* sf, hipStream_t stream);
+
+/* The values of moe_quantize_mxfp4's output: out [R, C] of out_dtype (BF16 or F32, both exact),
+ * 16-byte aligned; a block with scale byte 255 reads as NaN. */
+MOE_API moe_status_t moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int32_t R, int32_t C,
+                                          void* out, moe_dtype_t out_dtype, hipStream_t stream);
+
+/* Stacked expert weights to MXFP4 ("Mixture of Kittens", Step 8: the weights are pre-quantised
+ * once): blocks of 32 along the reduction, arithmetic as moe_quantize_mxfp4.
+ *  w [E, K, N] of w_dtype (BF16 or F32), K the reduction: the layout of the bf16 and fp32 experts;
+ *  layout MOE_MXFP4: q [E, N, K/2] out, or MOE_MXFP4_PAIRED: q [E, N/2, K/128, 2, 64] out
+ *  (K % 128 == 0 and N % 2 == 0), bitwise what moe_pack_mxfp4_pairs makes of the former;
+ *  sf [E, K/32, N] out in both. w and q 16-byte aligned, K % 32 == 0, E <= 65535. */
+MOE_API moe_status_t moe_quantize_mxfp4_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K,
+                                                int32_t N, moe_dtype_t layout, uint8_t* q, uint8_t* sf,
+                                                hipStream_t stream);
+
+/* The values of MXFP4 weights in either layout: out [E, K, N] of out_dtype (BF16 or F32, both
+ * exact); q and out 16-byte aligned. Limits as moe_quantize_mxfp4_weights. */
+MOE_API moe_status_t moe_dequantize_mxfp4_weights(const uint8_t* q, const uint8_t* sf, moe_dtype_t layout,
+                                                  int32_t E, int32_t K, int32_t N, void* out,
+                                                  moe_dtype_t out_dtype, hipStream_t stream);
 
 /* First half of the grouped expert FFN ("Mixture of Kittens", Step 1; "Distributed expert
  * parallelism", "Grouped expert computation"): for every expert e and its rows
@@ -353,6 +440,50 @@ MOE_API moe_status_t moe_grouped_ffn_fused_scatter(const void* x, moe_dtype_t ac
                                            int32_t E, int32_t H, int32_t Hp, const void* w_gate,
                                            const void* w_up, const void* w_down, moe_dtype_t wgt,
                                            const float* row_w, float* acc, void* ws, size_t ws_bytes,
+                                           hipStream_t stream);
+
+/* The two halves of the expert FFN with both operands in MXFP4 ("Mixture of Kittens", Step 8,
+ * low-precision expert GEMMs; DeepGEMM's Mega-MoE how-to: block-scaled GEMMs with the activations
+ * between them requantised): for every expert e and its rows r in [cu_seqlens[e],
+ * cu_seqlens[e+1]), with x the row's activations,
+ *     gate_up:  h[r] = silu(x . Wg[e]) * (x . Wu[e]),  stored as MXFP4 (h_q, h_sf)
+ *     down:     y_rows[r] = h[r] . Wd[e],  bf16
+ * accumulated in fp32; h is rounded to MXFP4 once, from its fp32 value, in blocks of 32 columns
+ * (arithmetic as moe_quantize_mxfp4).
+ *  x_q [T, H/2], x_sf [T, H/32] from moe_quantize_mxfp4, read through row_src [M] (row r is
+ *  token row_src[r] / K; -1: a padding row, zeros), or, with row_src NULL, [M, H/2] and
+ *  [M, H/32] rows in group order (T and K are then not used);
+ *  w_gate, w_up [E, Hp, H/2], w_down [E, H, Hp/2], scales sf_gate, sf_up [E, H/32, Hp] and
+ *  sf_down [E, Hp/32, H] in the MOE_MXFP4 layout (not the paired one);
+ *  h_q [M, Hp/2], h_sf [M, Hp/32]; y_rows [M, H] bf16. Rows past cu_seqlens[E] are not written.
+ *  Every pointer to codes 16-byte aligned, scales and y_rows too.
+ * Needs H % 128 == 0 and Hp % 128 == 0, E <= 1024, and T*H/2 and H*Hp/2 (the codes of x and of an
+ * expert matrix) below 2^31 (MOE_EUNSUPPORTED otherwise). One kernel launch each; with few rows per expert a kernel
+ * that streams the weights past the rows, else tiles on the matrix cores, with the same result
+ * up to the order of the fp32 sums. */
+MOE_API moe_status_t moe_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int32_t* row_src,
+                                           int32_t T, int32_t K, const int32_t* cu_seqlens, int32_t M,
+                                           int32_t E, int32_t H, int32_t Hp, const uint8_t* w_gate,
+                                           const uint8_t* w_up, const uint8_t* sf_gate,
+                                           const uint8_t* sf_up, uint8_t* h_q, uint8_t* h_sf,
+                                           hipStream_t stream);
+
+MOE_API moe_status_t moe_ffn_down_mxfp4(const uint8_t* h_q, const uint8_t* h_sf, const int32_t* cu_seqlens,
+                                        int32_t M, int32_t E, int32_t H, int32_t Hp, const uint8_t* w_down,
+                                        const uint8_t* sf_down, void* y_rows, hipStream_t stream);
+
+/* Scratch bytes of moe_grouped_ffn_mxfp4: h_q at offset 0, h_sf at the next multiple of 256
+ * (0 for invalid sizes). */
+MOE_API size_t moe_grouped_ffn_mxfp4_workspace_bytes(int32_t M, int32_t Hp);
+
+/* moe_ffn_gate_up_mxfp4 followed by moe_ffn_down_mxfp4, with h kept in `ws` (16-byte aligned).
+ * Calls that share a workspace must be ordered. */
+MOE_API moe_status_t moe_grouped_ffn_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int32_t* row_src,
+                                           int32_t T, int32_t K, const int32_t* cu_seqlens, int32_t M,
+                                           int32_t E, int32_t H, int32_t Hp, const uint8_t* w_gate,
+                                           const uint8_t* w_up, const uint8_t* w_down,
+                                           const uint8_t* sf_gate, const uint8_t* sf_up,
+                                           const uint8_t* sf_down, void* y_rows, void* ws, size_t ws_bytes,
                                            hipStream_t stream);
 
 /* Combine ("Distributed expert parallelism", lifecycle item 8 and "A four-rank example";

@@ -23,15 +23,21 @@ MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4, MOE_MXFP4_PAIRED = range(5)
 # moe_combine_t
 MOE_COMBINE_GATHER, MOE_COMBINE_SCATTER_ATOMIC = range(2)
 
+# moe_score_t
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = range(2)
+
 # offsets reported by moe_layer_workspace_layout, in order
 WS_FIELDS = ("topk_idx", "topk_w", "counts", "cu_seqlens", "pos", "row_src", "row_w", "x_perm",
              "x_perm_sf", "h", "h_sf", "y_rows", "permute_scratch", "acc_f32", "x_q", "x_q_sf",
              "fused_ctl")
 
-EXPORTS = ("moe_route_topk", "moe_permute_workspace_bytes", "moe_permute", "moe_permute_noalloc",
+EXPORTS = ("moe_route_topk", "moe_route_scored", "moe_route_scored_backward", "moe_permute_workspace_bytes", "moe_permute", "moe_permute_noalloc",
            "moe_padded_capacity",
            "moe_permute_padded", "moe_route_permute", "moe_quantize_fp8", "moe_pack_mxfp4_pairs", "moe_ffn_gate_up",
            "moe_ffn_gate_up_gather", "moe_ffn_down", "moe_ffn_down_scatter",
+           "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_quantize_mxfp4_weights",
+           "moe_dequantize_mxfp4_weights", "moe_ffn_gate_up_mxfp4", "moe_ffn_down_mxfp4",
+           "moe_grouped_ffn_mxfp4_workspace_bytes", "moe_grouped_ffn_mxfp4",
            "moe_grouped_ffn_workspace_bytes", "moe_grouped_ffn",
            "moe_grouped_ffn_fused_workspace_bytes", "moe_grouped_ffn_fused",
            "moe_grouped_ffn_fused_scatter", "moe_combine",
@@ -52,6 +58,13 @@ class LayerDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("Hp", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int),
                 ("wgt", ctypes.c_int), ("out", ctypes.c_int), ("combine", ctypes.c_int)]
+
+
+class RouteDesc(ctypes.Structure):
+    """moe_route_desc_t."""
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("score", ctypes.c_int), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -99,6 +112,17 @@ _SIGS = {
     "moe_layer_shared_workspace_bytes": (_S, [ctypes.POINTER(LayerDesc), _I]),
     "moe_layer_forward_shared": (_I, [ctypes.POINTER(LayerDesc), _I, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P, _P]),
+    "moe_route_scored": (_I, [ctypes.POINTER(RouteDesc), _P, _E, _P, _P, _P, _P]),
+    "moe_route_scored_backward": (_I, [ctypes.POINTER(RouteDesc), _P, _E, _P, _P, _P, _P]),
+    "moe_quantize_mxfp4": (_I, [_P, _E, _I, _I, _P, _P, _P]),
+    "moe_dequantize_mxfp4": (_I, [_P, _P, _I, _I, _P, _E, _P]),
+    "moe_quantize_mxfp4_weights": (_I, [_P, _E, _I, _I, _I, _E, _P, _P, _P]),
+    "moe_dequantize_mxfp4_weights": (_I, [_P, _P, _E, _I, _I, _I, _P, _E, _P]),
+    "moe_ffn_gate_up_mxfp4": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_ffn_down_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_grouped_ffn_mxfp4_workspace_bytes": (_S, [_I, _I]),
+    "moe_grouped_ffn_mxfp4": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S,
+                                   _P]),
     "moe_status_str": (ctypes.c_char_p, [_I]),
 }
 
@@ -153,6 +177,18 @@ def moe_route_topk(logits, T, E, K, topk_idx, topk_w, stream=None):
                                 _stream(stream)), "moe_route_topk")
 
 
+def moe_route_scored(desc: RouteDesc, logits, logits_dtype, bias, topk_idx, topk_w, stream=None):
+    _check(lib().moe_route_scored(ctypes.byref(desc), _ptr(logits), logits_dtype, _ptr(bias),
+                                  _ptr(topk_idx), _ptr(topk_w), _stream(stream)), "moe_route_scored")
+
+
+def moe_route_scored_backward(desc: RouteDesc, logits, logits_dtype, topk_idx, d_topk_w, d_logits,
+                              stream=None):
+    _check(lib().moe_route_scored_backward(ctypes.byref(desc), _ptr(logits), logits_dtype,
+                                           _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_logits),
+                                           _stream(stream)), "moe_route_scored_backward")
+
+
 def moe_permute_workspace_bytes(T, E, K) -> int:
     return int(lib().moe_permute_workspace_bytes(T, E, K))
 
@@ -202,6 +238,50 @@ def moe_quantize_fp8(x, x_dtype, R, C, q, sf, stream=None):
 def moe_pack_mxfp4_pairs(w, w_paired, E, N, K, stream=None):
     _check(lib().moe_pack_mxfp4_pairs(_ptr(w), _ptr(w_paired), E, N, K, _stream(stream)),
            "moe_pack_mxfp4_pairs")
+
+
+def moe_quantize_mxfp4(x, x_dtype, R, C, q, sf, stream=None):
+    _check(lib().moe_quantize_mxfp4(_ptr(x), x_dtype, R, C, _ptr(q), _ptr(sf), _stream(stream)),
+           "moe_quantize_mxfp4")
+
+
+def moe_dequantize_mxfp4(q, sf, R, C, out, out_dtype, stream=None):
+    _check(lib().moe_dequantize_mxfp4(_ptr(q), _ptr(sf), R, C, _ptr(out), out_dtype, _stream(stream)),
+           "moe_dequantize_mxfp4")
+
+
+def moe_quantize_mxfp4_weights(w, w_dtype, E, K, N, layout, q, sf, stream=None):
+    _check(lib().moe_quantize_mxfp4_weights(_ptr(w), w_dtype, E, K, N, layout, _ptr(q), _ptr(sf),
+                                            _stream(stream)), "moe_quantize_mxfp4_weights")
+
+
+def moe_dequantize_mxfp4_weights(q, sf, layout, E, K, N, out, out_dtype, stream=None):
+    _check(lib().moe_dequantize_mxfp4_weights(_ptr(q), _ptr(sf), layout, E, K, N, _ptr(out), out_dtype,
+                                              _stream(stream)), "moe_dequantize_mxfp4_weights")
+
+
+def moe_ffn_gate_up_mxfp4(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up,
+                          h_q, h_sf, stream=None):
+    _check(lib().moe_ffn_gate_up_mxfp4(_ptr(x_q), _ptr(x_sf), _ptr(row_src), T, K, _ptr(cu_seqlens), M, E,
+                                       H, Hp, _ptr(w_gate), _ptr(w_up), _ptr(sf_gate), _ptr(sf_up),
+                                       _ptr(h_q), _ptr(h_sf), _stream(stream)), "moe_ffn_gate_up_mxfp4")
+
+
+def moe_ffn_down_mxfp4(h_q, h_sf, cu_seqlens, M, E, H, Hp, w_down, sf_down, y_rows, stream=None):
+    _check(lib().moe_ffn_down_mxfp4(_ptr(h_q), _ptr(h_sf), _ptr(cu_seqlens), M, E, H, Hp, _ptr(w_down),
+                                    _ptr(sf_down), _ptr(y_rows), _stream(stream)), "moe_ffn_down_mxfp4")
+
+
+def moe_grouped_ffn_mxfp4_workspace_bytes(M, Hp) -> int:
+    return int(lib().moe_grouped_ffn_mxfp4_workspace_bytes(M, Hp))
+
+
+def moe_grouped_ffn_mxfp4(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, w_down, sf_gate,
+                          sf_up, sf_down, y_rows, ws, ws_bytes, stream=None):
+    _check(lib().moe_grouped_ffn_mxfp4(_ptr(x_q), _ptr(x_sf), _ptr(row_src), T, K, _ptr(cu_seqlens), M, E, H,
+                                       Hp, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(sf_gate),
+                                       _ptr(sf_up), _ptr(sf_down), _ptr(y_rows), _ptr(ws), ws_bytes,
+                                       _stream(stream)), "moe_grouped_ffn_mxfp4")
 
 
 def moe_ffn_gate_up(x_perm, x_perm_sf, act, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up,

@@ -1,0 +1,308 @@
+// Grouped expert FFN with both operands in MXFP4, on gfx950's block-scaled matrix cores.
+//
+//   gate/up:  h = silu(x.Wg) * (x.Wu), fp32, rounded in the epilogue to MXFP4 (mxfp4.h)
+//   down:     y = h.Wd, bf16
+//
+// MFMA v_mfma_scale_f32_32x32x64_f8f6f4 with two fp4 operands. A lane in group G = lane / 32
+// holds 16 bytes, 32 consecutive k of its row (or column), and the scale byte of that block.
+// Which 32 k of a stage a group takes is free as long as both operands agree: MFMA step kk of a
+// 256-wide stage takes block 4G + kk, so a lane's four steps read 64 neighbouring bytes and
+// their four scale bytes are one dword of the row's scales, picked by the instruction's byte
+// select.
+//
+// Tiles: 256 rows x 256 weight columns (128 of gate and the same 128 of up), 8 waves of 64 rows
+// x 128 columns, K stages of 256 (128 bytes of codes per row and per column: whole cache lines in
+// the stored layout), two stages in LDS filled by direct global->LDS loads, one in flight while
+// the other is consumed. Persistent grid, XCD-contiguous tile order and row blocks as in the fp8
+// kernel. Both operands are staged [256][128 B] with 16-byte chunk ^ (row/2 mod 8). A last half stage (K % 256
+// == 128) loads zeros for its absent blocks, codes and scales both.
+#include "lds_dma.h"
+#include "mxfp4.h"
+#include "tile_sched.h"
+
+#include <type_traits>
+
+namespace moe {
+
+namespace {
+
+constexpr int M4_BM = 256;
+constexpr int M4_BN = 256;      // weight columns per tile over both matrices
+constexpr int M4_BK = 256;
+constexpr int M4_NS = 2;
+constexpr int M4_THREADS = 512;
+constexpr int M4_MAX_E = 1024;
+constexpr int M4_OUT = (int)0x80000000u;  // an offset past every range: loads zeros
+
+constexpr int M4_A_BYTES = M4_BM * M4_BK / 2;
+constexpr int M4_B_BYTES = M4_BN * M4_BK / 2;
+constexpr int M4_LD = M4_A_BYTES / (1024 * 8);   // wave loads per stage, each operand
+constexpr int M4_SF_A = M4_A_BYTES + M4_B_BYTES;  // activation scales [256][8]
+constexpr int M4_SF_B = M4_SF_A + M4_BM * 8;      // weight scales [8][BN per matrix] per matrix
+constexpr int M4_STAGE = M4_SF_B + M4_BN * 8;
+constexpr int M4_LDS = M4_NS * M4_STAGE + (M4_MAX_E + 1 + 16) * 4;
+static_assert(M4_LDS <= 160 * 1024, "LDS budget");
+
+struct Mx4Args {
+  const uint8_t *A, *A_sf;
+  const int* row_src;  // gate/up only: rows gathered from A [a_rows]
+  int a_k, a_rows;
+  const int* cu;
+  int E, Kd, N;
+  const uint8_t *B0, *B0_sf, *B1, *B1_sf;
+  uint8_t *h_q, *h_sf;
+  uint16_t* y;
+};
+
+template <bool GATED>
+__global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
+  constexpr int NB = GATED ? 2 : 1;
+  constexpr int BN = M4_BN / NB;   // columns per matrix
+  constexpr int NT = BN / 64;      // 32-column blocks of a wave per matrix
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  int* tstart = reinterpret_cast<int*>(smem + M4_NS * M4_STAGE);
+  int* wsum = tstart + M4_MAX_E + 1;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int Kd = a.Kd, N = a.N;
+  const int ntn = (N + BN - 1) / BN;
+  const int total = build_tile_prefix<M4_BM, M4_THREADS>(a.cu, a.E, ntn, tstart, wsum);
+  const int kb = Kd / 2, ksf = Kd / 32;
+  const int nk = (Kd + M4_BK - 1) / M4_BK;
+  const bool half = Kd % M4_BK != 0;
+  const int G = gridDim.x;
+  const int slot = xcd_slot(blockIdx.x, G);
+  const uint32_t lds0 = lds_addr(smem);
+
+  // Loads of a stage: wave load j = wave + 8 i covers rows (columns) 8j..8j+7, lane -> row 8j + lane/8, slot
+  // lane % 8 of which holds chunk slot ^ (row/2 mod 8). Chunks 4..7 are absent in a half stage.
+  int ld_row[M4_LD], ld_chunk[M4_LD];
+#pragma unroll
+  for (int i = 0; i < M4_LD; ++i) {
+    ld_row[i] = (wave + 8 * i) * 8 + (lane >> 3);
+    ld_chunk[i] = (lane & 7) ^ ((ld_row[i] >> 1) & 7);
+  }
+  // Scales: of the rows, dword lane % 2 of row 32 wave + lane / 2; of the columns, LDS [NB][8][BN], bytes
+  // 256 wave .. of the block.
+  const int sa_row = wave * 32 + (lane >> 1), sa_half = lane & 1;
+  const int sb_byte = wave * 256 + lane * 4;
+  const int sb_nb = sb_byte / (8 * BN), sb_kb = (sb_byte / BN) & 7, sb_col = sb_byte % BN;
+
+  struct Tile {
+    int e, row0, rows_valid, n0, nmt;
+    i32x4_t rA, rS, rB0, rB1;
+    int a_off[M4_LD], s_off;
+  };
+  auto decode = [&](int t) __attribute__((always_inline)) {
+    Tile d;
+    d.e = __builtin_amdgcn_readfirstlane(find_expert(tstart, a.E, t));
+    const int lt = t - tstart[d.e];
+    const int gbeg = a.cu[d.e];
+    const int rows_e = a.cu[d.e + 1] - gbeg;
+    const int mte = (rows_e + M4_BM - 1) / M4_BM;
+    const int ntile = lt / mte;
+    const int mtile = lt - ntile * mte;
+    const int chunk = even_chunk(rows_e, mte);
+    d.row0 = __builtin_amdgcn_readfirstlane(gbeg + mtile * chunk);
+    d.rows_valid = __builtin_amdgcn_readfirstlane(min(chunk, rows_e - mtile * chunk));
+    d.n0 = __builtin_amdgcn_readfirstlane(ntile * BN);
+    if (GATED && a.row_src) {
+      d.rA = make_rsrc(a.A, (uint32_t)a.a_rows * (uint32_t)kb);
+      d.rS = make_rsrc(a.A_sf, (uint32_t)a.a_rows * (uint32_t)ksf);
+      int src[M4_LD];
+#pragma unroll
+      for (int i = 0; i < M4_LD; ++i) src[i] = a.row_src[d.row0 + min(ld_row[i], d.rows_valid - 1)];
+      const int ssrc = a.row_src[d.row0 + min(sa_row, d.rows_valid - 1)];
+#pragma unroll
+      for (int i = 0; i < M4_LD; ++i)
+        d.a_off[i] = (ld_row[i] < d.rows_valid && src[i] >= 0) ? (src[i] / a.a_k) * kb + ld_chunk[i] * 16 : M4_OUT;
+      d.s_off = (sa_row < d.rows_valid && ssrc >= 0) ? (ssrc / a.a_k) * ksf + sa_half * 4 : M4_OUT;
+    } else {
+      d.rA = make_rsrc(a.A + (size_t)d.row0 * kb, (uint32_t)d.rows_valid * (uint32_t)kb);
+      d.rS = make_rsrc(a.A_sf + (size_t)d.row0 * ksf, (uint32_t)d.rows_valid * (uint32_t)ksf);
+#pragma unroll
+      for (int i = 0; i < M4_LD; ++i)
+        d.a_off[i] = ld_row[i] < d.rows_valid ? ld_row[i] * kb + ld_chunk[i] * 16 : M4_OUT;
+      d.s_off = sa_row < d.rows_valid ? sa_row * ksf + sa_half * 4 : M4_OUT;
+    }
+    d.nmt = __builtin_amdgcn_readfirstlane((wm * 32 < d.rows_valid) + (128 + wm * 32 < d.rows_valid));
+    const size_t wbase = ((size_t)d.e * N + d.n0) * kb;
+    const uint32_t range = (uint32_t)(N - d.n0) * (uint32_t)kb;
+    d.rB0 = make_rsrc(a.B0 + wbase, range);
+    d.rB1 = GATED ? make_rsrc(a.B1 + wbase, range) : d.rB0;
+    return d;
+  };
+  auto issue = [&](const Tile& d, int kt, int buf) __attribute__((always_inline)) {
+    const uint32_t so = lds0 + (uint32_t)buf * M4_STAGE;
+    const bool cut = half && kt == nk - 1;
+#pragma unroll
+    for (int i = 0; i < M4_LD; ++i)
+      lds_dma16(d.rA, so + (wave + 8 * i) * 1024, cut && ld_chunk[i] >= 4 ? M4_OUT : d.a_off[i], kt * (M4_BK / 2));
+#pragma unroll
+    for (int i = 0; i < M4_LD; ++i) {
+      const bool second = GATED && i >= M4_LD / 2;
+      const int c = ld_row[i] - (second ? BN : 0);
+      lds_dma16(second ? d.rB1 : d.rB0, so + M4_A_BYTES + (wave + 8 * i) * 1024,
+                cut && ld_chunk[i] >= 4 ? M4_OUT : c * kb + ld_chunk[i] * 16, kt * (M4_BK / 2));
+    }
+    lds_dma4(d.rS, so + M4_SF_A + wave * 256, cut && sa_half ? M4_OUT : d.s_off, kt * 8);
+    const int planes = min(8, ksf - 8 * kt);
+    const uint8_t* sfb = (GATED && sb_nb) ? a.B1_sf : a.B0_sf;
+    lds_dma4(make_rsrc(sfb + ((size_t)d.e * ksf + 8 * (size_t)kt) * N, (uint32_t)N * (uint32_t)planes),
+             so + M4_SF_B + wave * 256, sb_kb < planes && d.n0 + sb_col < N ? sb_kb * N + d.n0 + sb_col : M4_OUT, 0);
+  };
+
+  // Fragments: row (column) block + lane % 32, chunk 4G + kk.
+  const int g2 = lane >> 5, l32 = lane & 31;
+  const int ar = wm * 32 + l32;
+  const int sw = (l32 >> 1) & 7;  // the same for every 32-row block
+  int f_off[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) f_off[kk] = ((4 * g2 + kk) ^ sw) << 4;
+
+  int buf = 0;
+  Tile cur;
+  if (slot < total) {
+    cur = decode(slot);
+    issue(cur, 0, 0);
+  }
+  for (int t = slot; t < total; t += G) {
+    f32x16_t acc[NB][2][NT];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[nb][mt][nt][i] = 0.f;
+
+    auto k_loop = [&](auto mtv) {
+      constexpr int MTV = decltype(mtv)::value;
+      for (int kt = 0; kt < nk; ++kt) {
+        // stage kt has landed for every wave, and every wave is done with the other buffer
+        wait_barrier<0>();
+        if (kt + 1 < nk) issue(cur, kt + 1, buf ^ 1);
+        if constexpr (MTV > 0) {
+          const unsigned char* st = smem + buf * M4_STAGE;
+          int sa[MTV];
+#pragma unroll
+          for (int mt = 0; mt < MTV; ++mt)
+            sa[mt] = *reinterpret_cast<const int*>(st + M4_SF_A + (mt * 128 + ar) * 8 + 4 * g2);
+          auto step = [&](auto kk_) __attribute__((always_inline)) {
+            constexpr int kk = decltype(kk_)::value;
+            const i32x4_t z = {0, 0, 0, 0};
+            i32x8_t af[MTV];
+#pragma unroll
+            for (int mt = 0; mt < MTV; ++mt)
+              af[mt] = __builtin_shufflevector(
+                  *reinterpret_cast<const i32x4_t*>(st + (mt * 128 + ar) * 128 + f_off[kk]), z, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const int c = wn * (BN / 2) + nt * 32 + l32;
+                const i32x8_t bf = __builtin_shufflevector(
+                    *reinterpret_cast<const i32x4_t*>(st + M4_A_BYTES + (nb * BN + c) * 128 + f_off[kk]), z, 0, 1, 2, 3,
+                    4, 5, 6, 7);
+                const int sb = st[M4_SF_B + (nb * 8 + 4 * g2 + kk) * BN + c];
+#pragma unroll
+                for (int mt = 0; mt < MTV; ++mt)  // weights first: lane l holds row l % 32 of the output
+                  acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af[mt], acc[nb][mt][nt], 4, 4, 0,
+                                                                                   sb, kk, sa[mt]);
+              }
+          };
+          step(std::integral_constant<int, 0>{});
+          step(std::integral_constant<int, 1>{});
+          step(std::integral_constant<int, 2>{});
+          step(std::integral_constant<int, 3>{});
+        }
+        buf ^= 1;
+      }
+    };
+    if (cur.nmt == 2) k_loop(std::integral_constant<int, 2>{});
+    else if (cur.nmt == 1) k_loop(std::integral_constant<int, 1>{});
+    else k_loop(std::integral_constant<int, 0>{});
+
+    const int row0 = cur.row0, rows_valid = cur.rows_valid, n0 = cur.n0;
+    // The next tile's first stage goes into the buffer that stage nk-1 did not use, whose readers all
+    // passed the last barrier.
+    if (t + G < total) {
+      cur = decode(t + G);
+      issue(cur, 0, buf);
+    }
+
+    // Lane l holds row l % 32 of its block; acc[..][4j + c] is column 8j + 4G + c of 32.
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const int r = mt * 128 + ar;
+      const bool ok = r < rows_valid;
+      const size_t row = (size_t)row0 + (ok ? r : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int c0 = n0 + wn * (BN / 2) + nt * 32;
+        if constexpr (GATED) {
+          // a block of 32 columns is the lane's 16 values and lane ^ 32's
+          float v[16];
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] = silu_f32(acc[0][mt][nt][i]) * acc[1][mt][nt][i];
+            m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+          }
+          const auto sw32 = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+          const uint32_t byte = mx_scale_byte(max((uint32_t)sw32[0], (uint32_t)sw32[1]));
+          // two runs of four columns per word, columns 8j + 4G; then the halves trade so that group 0 has
+          // columns 0..15 and group 1 columns 16..31
+          const uint32_t w0 = mx_pack8(v, byte), w1 = mx_pack8(v + 8, byte);
+          const auto tr = __builtin_amdgcn_permlane32_swap(w0, w1, false, false);
+          // tr[0]: columns 4.. of group 0's runs, tr[1]: of group 1's, interleaved by 16 bits
+          const uint32_t lo = __builtin_amdgcn_perm(tr[1], tr[0], 0x05040100);
+          const uint32_t hi = __builtin_amdgcn_perm(tr[1], tr[0], 0x07060302);
+          if (ok) {
+            *reinterpret_cast<uint2*>(a.h_q + row * (N / 2) + c0 / 2 + 8 * g2) = make_uint2(lo, hi);
+            if (g2 == 0) a.h_sf[row * (N / 32) + c0 / 32] = (uint8_t)byte;
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint4 v = pack_row16(acc[0][mt][nt], 8 * p);
+            if (ok && c0 < N) *reinterpret_cast<uint4*>(a.y + row * N + c0 + 16 * p + 8 * g2) = v;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool GATED>
+moe_status_t launch_tiles(const Mx4Args& a, hipStream_t s) {
+  static std::atomic<unsigned char> lds_set[MOE_MAX_DEVICES];
+  if (ensure_lds_limit(reinterpret_cast<const void*>(&ffn_mxfp4_kernel<GATED>), M4_LDS, lds_set) != MOE_OK)
+    return MOE_EHIP;
+  ffn_mxfp4_kernel<GATED><<<device_cu_count(), M4_THREADS, M4_LDS, s>>>(a);
+  return launch_status();
+}
+
+}  // namespace
+
+moe_status_t launch_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int* row_src, int T, int K,
+                                      const int* cu, int M, int E, int H, int Hp, const uint8_t* wg,
+                                      const uint8_t* wu, const uint8_t* sg, const uint8_t* su, uint8_t* h_q,
+                                      uint8_t* h_sf, hipStream_t s) {
+  if (M == 0) return MOE_OK;
+  const Mx4Args a{x_q, x_sf, row_src, K, T, cu, E, H, Hp, wg, sg, wu, su, h_q, h_sf, nullptr};
+  return launch_tiles<true>(a, s);
+}
+
+moe_status_t launch_ffn_down_mxfp4(const uint8_t* h_q, const uint8_t* h_sf, const int* cu, int M, int E, int H,
+                                   int Hp, const uint8_t* wd, const uint8_t* sd, void* y, hipStream_t s) {
+  if (M == 0) return MOE_OK;
+  const Mx4Args a{h_q, h_sf, nullptr, 1, 0, cu, E, Hp, H, wd, sd, nullptr, nullptr, nullptr, nullptr,
+                  static_cast<uint16_t*>(y)};
+  return launch_tiles<false>(a, s);
+}
+
+}  // namespace moe

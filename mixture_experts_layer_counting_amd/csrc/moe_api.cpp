@@ -35,6 +35,24 @@ moe_status_t launch_ffn_gate_up_fp8(const void*, const float*, const int*, int, 
 moe_status_t launch_ffn_down_fp8(const void*, const float*, const int*, int, int, int, int,
                                  const void*, const uint8_t*, void*, const RowMaps&, bool paired, hipStream_t);
 moe_status_t launch_pack_mxfp4_pairs(const void* w, void* out, int E, int N, int K, hipStream_t s);
+moe_status_t launch_route_scored(const moe_route_desc_t& d, const void* logits, moe_dtype_t lt, const float* bias,
+                                 int* topk_idx, float* topk_w, hipStream_t s);
+moe_status_t launch_route_scored_bwd(const moe_route_desc_t& d, const void* logits, moe_dtype_t lt,
+                                     const int* topk_idx, const float* d_topk_w, void* d_logits, hipStream_t s);
+moe_status_t launch_quantize_mxfp4(const void* x, moe_dtype_t xt, int R, int C, uint8_t* q, uint8_t* sf,
+                                   hipStream_t s);
+moe_status_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int R, int C, void* out,
+                                     moe_dtype_t ot, hipStream_t s);
+moe_status_t launch_quantize_mxfp4_weights(const void* w, moe_dtype_t wt, int E, int K, int N, bool paired,
+                                           uint8_t* q, uint8_t* sf, hipStream_t s);
+moe_status_t launch_dequantize_mxfp4_weights(const uint8_t* q, const uint8_t* sf, bool paired, int E, int K, int N,
+                                             void* out, moe_dtype_t ot, hipStream_t s);
+moe_status_t launch_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int* row_src, int T, int K,
+                                      const int* cu, int M, int E, int H, int Hp, const uint8_t* wg,
+                                      const uint8_t* wu, const uint8_t* sg, const uint8_t* su, uint8_t* h_q,
+                                      uint8_t* h_sf, hipStream_t s);
+moe_status_t launch_ffn_down_mxfp4(const uint8_t* h_q, const uint8_t* h_sf, const int* cu, int M, int E, int H,
+                                   int Hp, const uint8_t* wd, const uint8_t* sd, void* y, hipStream_t s);
 moe_status_t launch_ffn_gate_up_f32(const void*, const int*, int, int, int, int, const void*,
                                     const void*, void*, const RowMaps&, hipStream_t);
 moe_status_t launch_ffn_down_f32(const void*, const int*, int, int, int, int, const void*, void*,
@@ -168,6 +186,38 @@ moe_status_t moe_route_topk(const float* logits, int32_t T, int32_t E, int32_t K
   return launch_route_topk(logits, T, E, K, topk_idx, topk_w, stream);
 }
 
+// Sizes and dtype of a moe_route_scored call.
+static moe_status_t check_route_desc(const moe_route_desc_t* d, moe_dtype_t lt) {
+  if (!d || d->T < 0 || d->E < 1 || d->K < 1 || d->groups < 1 || d->topk_groups < 1) return MOE_EINVAL;
+  if (d->score != MOE_SCORE_SOFTMAX && d->score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+  if (d->renorm != 0 && d->renorm != 1) return MOE_EINVAL;
+  if (!(d->scale - d->scale == 0.0f)) return MOE_EINVAL;
+  if (d->E % d->groups || d->topk_groups > d->groups) return MOE_EINVAL;
+  const int size = d->E / d->groups;
+  if (d->group_top < 1 || d->group_top > 2 || d->group_top > size) return MOE_EINVAL;
+  if (d->K > (int64_t)d->topk_groups * size) return MOE_EINVAL;
+  if (d->K > 32 || d->E > 1024 || d->groups > 64) return MOE_EUNSUPPORTED;
+  if (lt != MOE_F32 && lt != MOE_BF16) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_route_scored(const moe_route_desc_t* d, const void* logits, moe_dtype_t logits_dtype,
+                              const float* bias, int32_t* topk_idx, float* topk_w, hipStream_t stream) {
+  const moe_status_t st = check_route_desc(d, logits_dtype);
+  if (st != MOE_OK) return st;
+  if (d->T > 0 && (!logits || !topk_idx || !topk_w)) return MOE_EINVAL;
+  return launch_route_scored(*d, logits, logits_dtype, bias, topk_idx, topk_w, stream);
+}
+
+moe_status_t moe_route_scored_backward(const moe_route_desc_t* d, const void* logits, moe_dtype_t logits_dtype,
+                                       const int32_t* topk_idx, const float* d_topk_w, void* d_logits,
+                                       hipStream_t stream) {
+  const moe_status_t st = check_route_desc(d, logits_dtype);
+  if (st != MOE_OK) return st;
+  if (d->T > 0 && (!logits || !topk_idx || !d_topk_w || !d_logits)) return MOE_EINVAL;
+  return launch_route_scored_bwd(*d, logits, logits_dtype, topk_idx, d_topk_w, d_logits, stream);
+}
+
 size_t moe_permute_workspace_bytes(int32_t T, int32_t E, int32_t K) {
   if (T < 0 || E < 1 || K < 1) return 0;
   return permute_ws_bytes(T, E, K);
@@ -291,6 +341,136 @@ moe_status_t moe_pack_mxfp4_pairs(const uint8_t* w, uint8_t* w_paired, int32_t E
   if (!w || !w_paired || w == w_paired) return MOE_EINVAL;
   if ((uintptr_t)w % 16 || (uintptr_t)w_paired % 16) return MOE_EINVAL;
   return launch_pack_mxfp4_pairs(w, w_paired, E, N, K, stream);
+}
+
+static bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+// R x C values of blocks of 32, in one launch of eight values per lane.
+static moe_status_t check_mxfp4_rows(moe_dtype_t dt, int64_t R, int64_t C) {
+  if (R < 0 || C < 1) return MOE_EINVAL;
+  if (C % 32 || (dt != MOE_BF16 && dt != MOE_F32)) return MOE_EUNSUPPORTED;
+  if (R * (C / 32) > (int64_t)std::numeric_limits<int32_t>::max() * 64) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_mxfp4(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t C, uint8_t* q,
+                                uint8_t* sf, hipStream_t stream) {
+  const moe_status_t st = check_mxfp4_rows(x_dtype, R, C);
+  if (st != MOE_OK) return st;
+  if (R > 0 && (!x || !q || !sf)) return MOE_EINVAL;
+  if (!aligned16(x) || (uintptr_t)q % 4) return MOE_EINVAL;
+  return launch_quantize_mxfp4(x, x_dtype, R, C, q, sf, stream);
+}
+
+moe_status_t moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, int32_t R, int32_t C, void* out,
+                                  moe_dtype_t out_dtype, hipStream_t stream) {
+  const moe_status_t st = check_mxfp4_rows(out_dtype, R, C);
+  if (st != MOE_OK) return st;
+  if (R > 0 && (!q || !sf || !out)) return MOE_EINVAL;
+  if (!aligned16(out) || (uintptr_t)q % 4) return MOE_EINVAL;
+  return launch_dequantize_mxfp4(q, sf, R, C, out, out_dtype, stream);
+}
+
+static moe_status_t check_mxfp4_weights(moe_dtype_t dt, moe_dtype_t layout, int E, int K, int N) {
+  if (E < 0 || K < 0 || N < 0) return MOE_EINVAL;
+  if (dt != MOE_BF16 && dt != MOE_F32) return MOE_EUNSUPPORTED;
+  if (layout != MOE_MXFP4 && layout != MOE_MXFP4_PAIRED) return MOE_EUNSUPPORTED;
+  if (K % 32 || E > 65535 || K / 256 >= 65535) return MOE_EUNSUPPORTED;
+  if (layout == MOE_MXFP4_PAIRED && (K % 128 || N % 2)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_mxfp4_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K, int32_t N,
+                                        moe_dtype_t layout, uint8_t* q, uint8_t* sf, hipStream_t stream) {
+  const moe_status_t st = check_mxfp4_weights(w_dtype, layout, E, K, N);
+  if (st != MOE_OK) return st;
+  if (E == 0 || K == 0 || N == 0) return MOE_OK;
+  if (!w || !q || !sf || !aligned16(w) || !aligned16(q)) return MOE_EINVAL;
+  return launch_quantize_mxfp4_weights(w, w_dtype, E, K, N, layout == MOE_MXFP4_PAIRED, q, sf, stream);
+}
+
+moe_status_t moe_dequantize_mxfp4_weights(const uint8_t* q, const uint8_t* sf, moe_dtype_t layout, int32_t E,
+                                          int32_t K, int32_t N, void* out, moe_dtype_t out_dtype,
+                                          hipStream_t stream) {
+  const moe_status_t st = check_mxfp4_weights(out_dtype, layout, E, K, N);
+  if (st != MOE_OK) return st;
+  if (E == 0 || K == 0 || N == 0) return MOE_OK;
+  if (!q || !sf || !out || !aligned16(q) || !aligned16(out)) return MOE_EINVAL;
+  return launch_dequantize_mxfp4_weights(q, sf, layout == MOE_MXFP4_PAIRED, E, K, N, out, out_dtype, stream);
+}
+
+// Sizes of the MXFP4 x MXFP4 FFN: offsets into one expert's codes and into a 256-row block are
+// 32-bit.
+static moe_status_t check_ffn_mxfp4(int64_t M, int E, int64_t H, int64_t Hp) {
+  if (M < 0 || E < 1 || H < 1 || Hp < 1) return MOE_EINVAL;
+  if (M > std::numeric_limits<int32_t>::max() / 2 || E > 1024) return MOE_EUNSUPPORTED;
+  if (H % 128 || Hp % 128) return MOE_EUNSUPPORTED;
+  if (H * Hp / 2 >= (1ll << 31) || 256 * (H > Hp ? H : Hp) / 2 >= (1ll << 31)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+static moe_status_t check_gather_mxfp4(const int32_t* row_src, int64_t T, int K, int64_t H) {
+  if (!row_src) return MOE_OK;
+  if (T < 0 || K < 1) return MOE_EINVAL;
+  return T * H / 2 >= (1ll << 31) ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+moe_status_t moe_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int32_t* row_src, int32_t T,
+                                   int32_t K, const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H,
+                                   int32_t Hp, const uint8_t* w_gate, const uint8_t* w_up,
+                                   const uint8_t* sf_gate, const uint8_t* sf_up, uint8_t* h_q, uint8_t* h_sf,
+                                   hipStream_t stream) {
+  moe_status_t st = check_ffn_mxfp4(M, E, H, Hp);
+  if (st == MOE_OK) st = check_gather_mxfp4(row_src, T, K, H);
+  if (st != MOE_OK) return st;
+  if (!cu_seqlens) return MOE_EINVAL;
+  if (M > 0 && (!x_q || !x_sf || !w_gate || !w_up || !sf_gate || !sf_up || !h_q || !h_sf)) return MOE_EINVAL;
+  if (!aligned16(x_q) || !aligned16(x_sf) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(sf_gate) ||
+      !aligned16(sf_up) || !aligned16(h_q) || !aligned16(h_sf))
+    return MOE_EINVAL;
+  return launch_ffn_gate_up_mxfp4(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up,
+                                  h_q, h_sf, stream);
+}
+
+moe_status_t moe_ffn_down_mxfp4(const uint8_t* h_q, const uint8_t* h_sf, const int32_t* cu_seqlens, int32_t M,
+                                int32_t E, int32_t H, int32_t Hp, const uint8_t* w_down, const uint8_t* sf_down,
+                                void* y_rows, hipStream_t stream) {
+  const moe_status_t st = check_ffn_mxfp4(M, E, H, Hp);
+  if (st != MOE_OK) return st;
+  if (!cu_seqlens) return MOE_EINVAL;
+  if (M > 0 && (!h_q || !h_sf || !w_down || !sf_down || !y_rows)) return MOE_EINVAL;
+  if (!aligned16(h_q) || !aligned16(h_sf) || !aligned16(w_down) || !aligned16(sf_down) || !aligned16(y_rows))
+    return MOE_EINVAL;
+  return launch_ffn_down_mxfp4(h_q, h_sf, cu_seqlens, M, E, H, Hp, w_down, sf_down, y_rows, stream);
+}
+
+size_t moe_grouped_ffn_mxfp4_workspace_bytes(int32_t M, int32_t Hp) {
+  if (M < 0 || Hp < 1 || Hp % 128) return 0;
+  return align_up((size_t)M * (Hp / 2), 256) + align_up((size_t)M * (Hp / 32), 256);
+}
+
+moe_status_t moe_grouped_ffn_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int32_t* row_src, int32_t T,
+                                   int32_t K, const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H,
+                                   int32_t Hp, const uint8_t* w_gate, const uint8_t* w_up, const uint8_t* w_down,
+                                   const uint8_t* sf_gate, const uint8_t* sf_up, const uint8_t* sf_down,
+                                   void* y_rows, void* ws, size_t ws_bytes, hipStream_t stream) {
+  moe_status_t st = check_ffn_mxfp4(M, E, H, Hp);
+  if (st == MOE_OK) st = check_gather_mxfp4(row_src, T, K, H);
+  if (st != MOE_OK) return st;
+  if (!cu_seqlens) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (ws_bytes < moe_grouped_ffn_mxfp4_workspace_bytes(M, Hp) || !ws) return MOE_EWORKSPACE;
+  for (const void* p : {(const void*)x_q, (const void*)x_sf, (const void*)w_gate, (const void*)w_up,
+                        (const void*)w_down, (const void*)sf_gate, (const void*)sf_up, (const void*)sf_down,
+                        (const void*)y_rows, (const void*)ws})
+    if (!p || !aligned16(p)) return MOE_EINVAL;
+  uint8_t* h_q = static_cast<uint8_t*>(ws);
+  uint8_t* h_sf = h_q + align_up((size_t)M * (Hp / 2), 256);
+  poison(ws, ws_bytes, stream);
+  st = moe_ffn_gate_up_mxfp4(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up, h_q,
+                             h_sf, stream);
+  if (st != MOE_OK) return st;
+  return moe_ffn_down_mxfp4(h_q, h_sf, cu_seqlens, M, E, H, Hp, w_down, sf_down, y_rows, stream);
 }
 
 moe_status_t moe_ffn_gate_up(const void* x_perm, const float* x_perm_sf, moe_dtype_t act,

@@ -178,7 +178,149 @@ def quantize_fp8_1x128(x: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
     return encode_e4m3fn(q.reshape(R, C)), s
 
 
+# ----------------------------------------------------------------------------- MXFP4
+
+
+E2M1_VALUES = decode_e2m1(np.arange(8))
+
+
+def round_e2m1(v: np.ndarray) -> np.ndarray:
+    """e2m1 codes (0..15) of the values nearest to v: ties to the even code, beyond 6 to 6."""
+    v = np.asarray(v, dtype=np.float64)
+    a = np.minimum(np.abs(v), 6.0)
+    dist = np.abs(a[..., None] - E2M1_VALUES)
+    best = dist.min(axis=-1, keepdims=True)
+    near = dist == best                                  # one code, or two neighbours at a tie
+    even = near & (np.arange(8) % 2 == 0)
+    code = np.where(even.any(axis=-1), even.argmax(axis=-1), near.argmax(axis=-1))
+    return (code | np.where(v < 0, 8, 0)).astype(np.uint8)
+
+
+def mxfp4_scale_byte(amax: np.ndarray) -> np.ndarray:
+    """e8m0 byte of a block (OCP Microscaling v1.0: X = 2^(floor(log2 amax) - 2), e2m1's largest
+    exponent being 2), at least 0; an all-zero block has byte 0, one with an infinity or a NaN
+    byte 255."""
+    amax = np.asarray(amax, dtype=np.float64)
+    ok = np.isfinite(amax) & (amax > 0)
+    _, e = np.frexp(np.where(ok, amax, 1.0))             # amax = m 2^e, m in [0.5, 1)
+    b = np.where(ok, np.maximum(e - 1 - 2 + 127, 0), 0)
+    return np.where(np.isfinite(amax), b, 255).astype(np.uint8)
+
+
+def quantize_mxfp4(x: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """Rows of x [R, C] -> (codes, two per byte, low nibble first [R, C/2]; scale bytes
+    [R, C/32]). Blocks with a NaN or an infinity: zero codes, byte 255."""
+    x = np.asarray(x, dtype=np.float64)
+    R, C = x.shape
+    blocks = x.reshape(R, C // 32, 32)
+    amax = np.abs(blocks).max(axis=2)                    # NaN stays NaN
+    byte = mxfp4_scale_byte(amax)
+    bad = byte == 255
+    v = np.where(bad[:, :, None], 0.0, blocks) / np.where(bad, 1.0, np.exp2(byte.astype(np.float64) - 127.0))[:, :, None]
+    code = round_e2m1(v).reshape(R, C // 2, 2)
+    return (code[..., 0] | (code[..., 1] << 4)).astype(np.uint8), byte
+
+
+def decode_mxfp4_rows(packed: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """codes [R, C/2] with scale bytes [R, C/32] -> float64 [R, C]."""
+    return decode_mxfp4(packed, np.asarray(scales).T).T
+
+
 # ----------------------------------------------------------------------------- routing
+
+
+def masked_logits(logits: np.ndarray, lowest: float) -> np.ndarray:
+    """Logits as float64 with masked experts (NaN, -inf, the storage type's lowest value) as
+    -inf and +inf as the largest fp32 value."""
+    l = np.asarray(logits, dtype=np.float64)
+    return np.where(l > lowest, np.minimum(l, np.finfo(np.float32).max.astype(np.float64)), -np.inf)
+
+
+def scores(l: np.ndarray, score: str) -> np.ndarray:
+    """sigmoid or softmax scores of masked_logits' rows, 0 for masked experts."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        if score == "sigmoid":
+            return 1.0 / (1.0 + np.exp(-l))
+        top = l.max(axis=1, keepdims=True)
+        z = np.exp(l - np.where(np.isfinite(top), top, 0.0))
+        total = z.sum(axis=1, keepdims=True)
+        return z / np.where(total > 0, total, 1.0)
+
+
+def route_scored(logits: np.ndarray, K: int, *, score: str, bias: Optional[np.ndarray] = None, groups: int = 1,
+                 topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+                 lowest: float = float(np.finfo(np.float32).min)) -> Tuple[np.ndarray, np.ndarray]:
+    """Routing by scores, one token at a time ("Mixture of Kittens", Step 1; "Distributed expert
+    parallelism", node-limited routing) -> (topk_idx int32 [T, K], topk_w float64). The choice is
+    the score plus the bias, or the logit without a bias; ties go to the lower id; picks that
+    are not there are -1 with weight 0."""
+    l = masked_logits(logits, lowest)
+    s = scores(l, score)
+    T, E = l.shape
+    size = E // groups
+    idx = np.full((T, K), -1, np.int32)
+    w = np.zeros((T, K))
+    for t in range(T):
+        live = l[t] > -np.inf
+        if bias is not None:
+            b = np.asarray(bias, np.float64)
+            live = live & (b > -np.inf)
+            c = s[t] + np.where(live, b, 0.0)
+        else:
+            c = l[t]
+        kept = range(groups)
+        if topk_groups < groups:
+            u = s[t] if bias is None and group_top == 2 else c
+            value = []
+            for g in range(groups):
+                best = sorted((u[e] for e in range(g * size, (g + 1) * size) if live[e]), reverse=True)[:group_top]
+                value.append(sum(best) if best else -np.inf)
+            kept = sorted(range(groups), key=lambda g: (-value[g], g))[:topk_groups]
+        can = [e for g in kept for e in range(g * size, (g + 1) * size) if live[e]]
+        picks = sorted(can, key=lambda e: (-c[e], e))[:K]
+        # a renormalised weight is a ratio: taken from the logs where the scores themselves underflow
+        p = np.array([s[t, e] for e in picks])
+        if renorm and picks:
+            if score == "sigmoid" and p.max() < 1e-30:
+                p = np.exp(l[t, picks] - l[t, picks].max())
+            if score == "softmax":
+                p = np.exp(l[t, picks] - l[t, picks].max())
+            p = p / p.sum()
+        idx[t, :len(picks)] = picks
+        w[t, :len(picks)] = scale * p
+    return idx, w
+
+
+def route_scored_backward(logits: np.ndarray, topk_idx: np.ndarray, d_topk_w: np.ndarray, *, score: str,
+                          renorm: bool = True, scale: float = 1.0,
+                          lowest: float = float(np.finfo(np.float32).min)) -> np.ndarray:
+    """d_logits [T, E] of route_scored for given picks (ids out of range and masked experts take
+    no part, an expert named twice counts twice)."""
+    l = masked_logits(logits, lowest)
+    s = scores(l, score)
+    T, E = l.shape
+    out = np.zeros((T, E))
+    for t in range(T):
+        picks = [(int(e), float(d)) for e, d in zip(topk_idx[t], d_topk_w[t])
+                 if 0 <= e < E and l[t, int(e)] > -np.inf]
+        if not picks:
+            continue
+        e = np.array([p[0] for p in picks])
+        d = np.array([p[1] for p in picks])
+        p = s[t, e]
+        with np.errstate(over="ignore"):
+            one_minus = 1.0 / (1.0 + np.exp(l[t, e]))
+        if renorm:
+            q = p if score == "sigmoid" and p.max() >= 1e-30 else np.exp(l[t, e] - l[t, e].max())
+            r = q / q.sum()
+            v = r * (d - (d * r).sum()) * (one_minus if score == "sigmoid" else 1.0)
+            np.add.at(out[t], e, scale * v)
+        elif score == "sigmoid":
+            np.add.at(out[t], e, scale * d * p * one_minus)
+        else:
+            np.add.at(out[t], e, scale * d * p)
+            out[t] -= scale * (d * p).sum() * s[t]
+    return out
 
 
 def route_topk(logits: np.ndarray, K: int) -> Tuple[np.ndarray, np.ndarray]:

@@ -1,0 +1,170 @@
+"""Routing by scores and its gradient against the float64 oracle. Picks are compared exactly.
+
+Tolerances, with u = 2^-24: a score errs by at most about 4 u of its value (expf and the division), a share of
+the picks by 12 u, and is at most 1, so weights lie within 16 u * scale < 1e-6 * scale. A gradient
+r (d - sum d r) (1 - s) adds the sum over at most 32 picks: (32 + 44) u max|d| on top of 12 u, below
+96 u * scale * max|d|. The dense softmax form multiplies by scores whose sum over E experts errs
+by (E / 64 + 6) u and whose exponent by |l - max| u, with s |l - max| < 0.37: within the same 96 u.
+bf16 gradients are rounded once more, by 2^-8 of their value."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_counting_amd as moe
+from oracle import moe_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+FMT = {"f32": (moe.MOE_F32, torch.float32), "bf16": (moe.MOE_BF16, torch.bfloat16)}
+
+
+def desc(T, E, K, score="sigmoid", groups=1, topk_groups=1, group_top=1, renorm=True, scale=1.0):
+    code = moe.MOE_SCORE_SIGMOID if score == "sigmoid" else moe.MOE_SCORE_SOFTMAX
+    return moe.RouteDesc(T, E, K, code, groups, topk_groups, group_top, int(renorm), scale)
+
+
+def run_route(lg, dtype, bias, K, **kw):
+    T, E = lg.shape
+    idx = torch.full((T, K), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, K), -7.0, device=DEV)
+    moe.moe_route_scored(desc(T, E, K, **kw), lg, FMT[dtype][0], bias, idx, w)
+    return idx, w
+
+
+def check(logits, dtype, K, bias=None, backward=True, seed=0, **kw):
+    print(f"[case] {tuple(logits.shape)} {dtype} K={K} bias={bias is not None} {kw}", flush=True)
+    lg = torch.from_numpy(logits).to(DEV).to(FMT[dtype][1]).contiguous()
+    b = None if bias is None else torch.from_numpy(bias).to(DEV)
+    idx, w = run_route(lg, dtype, b, K, **kw)
+    torch.cuda.synchronize()
+    stored = lg.float().cpu().numpy()
+    lowest = float(torch.finfo(FMT[dtype][1]).min)
+    ri, rw = O.route_scored(stored, K, bias=bias, lowest=lowest, **kw)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    scale = kw.get("scale", 1.0)
+    assert np.abs(w.cpu().numpy() - rw).max(initial=0) <= 1e-6 * scale
+    if not backward:
+        return
+    T, E = logits.shape
+    d = np.random.default_rng(seed).standard_normal((T, K)).astype(np.float32)
+    out = torch.full((T, E), 7.0, dtype=FMT[dtype][1], device=DEV)
+    moe.moe_route_scored_backward(desc(T, E, K, **kw), lg, FMT[dtype][0], idx, torch.from_numpy(d).to(DEV), out)
+    torch.cuda.synchronize()
+    ref = O.route_scored_backward(stored, ri, d, score=kw.get("score", "sigmoid"), renorm=kw.get("renorm", True),
+                                  scale=scale, lowest=lowest)
+    tol = 96 * U * scale * max(1.0, np.abs(d).max(initial=0)) + (2.0 ** -8 if dtype == "bf16" else 0) * np.abs(ref)
+    assert (np.abs(out.float().cpu().numpy() - ref) <= tol).all()
+
+
+FORMS = [dict(score=s, renorm=r, scale=c) for s, (r, c) in itertools.product(
+    ("sigmoid", "softmax"), ((True, 2.5), (False, 1.0)))]
+
+
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f"{f['score']}_{'renorm' if f['renorm'] else 'plain'}")
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,K,G,tg,top", [
+    (1, 1, 1, 1, 1, 1), (1, 64, 6, 1, 1, 1), (5, 2, 2, 2, 1, 1), (33, 7, 3, 1, 1, 1), (64, 60, 4, 6, 3, 2),
+    (129, 384, 8, 8, 4, 2), (70, 256, 8, 8, 4, 1), (17, 1024, 32, 64, 9, 2), (9, 1023, 5, 33, 7, 2), (31, 130, 16, 13, 13, 2),
+    (40, 96, 12, 3, 1, 2), (8, 961, 32, 31, 2, 1)])
+def test_route_scored(T, E, K, G, tg, top, dtype, form):
+    if form["score"] == "sigmoid" and tg * (E // G) < K or tg * (E // G) < K:
+        K = tg * (E // G)
+    rng = np.random.default_rng(T * 1000 + E)
+    lg = rng.standard_normal((T, E)).astype(np.float32) * 1.5
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    for b in (None, bias):
+        check(lg, dtype, K, b, groups=G, topk_groups=tg, group_top=top, **form)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("top", [1, 2])
+def test_near_and_equal_choices_are_ordered_as_in_binary64(score, top):
+    """Choices a few fp32 roundings apart, and exactly equal ones: the fp32 pass alone would order
+    some of them wrongly."""
+    rng = np.random.default_rng(11)
+    T, E, G = 200, 64, 4
+    base = rng.standard_normal((T, 1)).astype(np.float32)
+    lg = (base + (rng.integers(-3, 4, (T, E)) * 2.0 ** -22)).astype(np.float32)
+    bias = (rng.integers(-3, 4, E) * 2.0 ** -23).astype(np.float32)
+    for b in (bias, np.zeros(E, np.float32), None):
+        check(lg, "f32", 8, b, score=score, groups=G, topk_groups=2, group_top=top, renorm=True)
+        check(lg, "f32", 8, b, score=score, renorm=False)
+    # the bias undoes the scores' differences: choices equal to the last digits across experts
+    lg = np.tile(rng.standard_normal((1, E)).astype(np.float32), (3, 1))
+    s = O.scores(lg.astype(np.float64), score)[0]
+    check(lg, "f32", 8, (0.7 - s).astype(np.float32), score=score, renorm=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f"{f['score']}_{'renorm' if f['renorm'] else 'plain'}")
+@pytest.mark.parametrize("bias", [False, True])
+def test_masks(dtype, form, bias):
+    rng = np.random.default_rng(2)
+    T, E = 50, 40
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+    u = rng.random((T, E))
+    lg[u < 0.2] = -np.inf
+    lg[(u >= 0.2) & (u < 0.4)] = torch.finfo(FMT[dtype][1]).min
+    lg[(u >= 0.4) & (u < 0.6)] = np.nan
+    lg[(u >= 0.6) & (u < 0.62)] = np.inf
+    lg[7] = -np.inf                                   # nothing left
+    lg[8] = np.nan
+    lg[9] = -np.inf
+    lg[9, 13] = 0.5                                   # one expert left
+    lg[10] = -np.inf
+    lg[10, 20:22] = -80.0                              # far out: shares of scores near 1e-35
+    lg[11] = -np.inf
+    lg[11, 3:9] = [-3e38, 3e38, -100.0, 100.0, 0.0, -200.0]
+    b = None
+    if bias:
+        b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+        b[5], b[6] = -np.inf, np.nan
+    check(lg, dtype, 6, b, groups=4, topk_groups=2, group_top=2, **form)
+    check(lg, dtype, 6, b, **form)
+
+
+def test_sigmoid_shares_of_vanishing_scores():
+    lg = np.full((2, 8), -np.inf, np.float32)
+    lg[0, :4] = [-150.0, -151.0, -152.0, -200.0]
+    lg[1, :4] = [-60.0, -59.0, -61.0, -90.0]
+    check(lg, "f32", 4, score="sigmoid", renorm=True)
+
+
+def test_backward_takes_any_ids():
+    """Ids out of range take no part, even with NaN gradients; the same expert twice adds up."""
+    lg = np.random.default_rng(1).standard_normal((3, 20)).astype(np.float32)
+    ids = np.array([[3, 3, 7, -1], [20, 2 ** 31 - 1, -5, 0], [-1, -1, -1, -1]], np.int32)
+    d = np.array([[1.0, 2.0, -1.0, np.nan], [np.nan, 1.0, 1.0, 0.5], [1.0, 1.0, 1.0, 1.0]], np.float32)
+    for form in FORMS:
+        out = torch.full((3, 20), 7.0, device=DEV)
+        moe.moe_route_scored_backward(desc(3, 20, 4, **form), torch.from_numpy(lg).to(DEV), moe.MOE_F32,
+                                      torch.from_numpy(ids).to(DEV), torch.from_numpy(d).to(DEV), out)
+        torch.cuda.synchronize()
+        ref = O.route_scored_backward(lg, ids, d, **form)
+        assert np.abs(out.cpu().numpy() - ref).max() <= 96 * U * form["scale"] * 3
+
+
+def test_unaligned_rows_and_buffers():
+    """Buffers that start 4 (fp32) or 2 (bf16) bytes past a 16-byte line, rows of any length."""
+    for dtype in ("f32", "bf16"):
+        for E in (12, 16, 21):
+            T, K = 9, 3
+            flat = torch.randn(T * E + 1, device=DEV).to(FMT[dtype][1])
+            lg = flat[1:].view(T, E)
+            idx, w = run_route(lg, dtype, None, K)
+            g = torch.full((T * E + 2,), 5.0, dtype=FMT[dtype][1], device=DEV)
+            d = torch.ones(T, K, device=DEV)
+            d[:, 0] = 2.0
+            moe.moe_route_scored_backward(desc(T, E, K), lg, FMT[dtype][0], idx, d, g[1:-1].view(T, E))
+            torch.cuda.synchronize()
+            stored = lg.float().cpu().numpy()
+            ri, _ = O.route_scored(stored, K, score="sigmoid")
+            assert np.array_equal(idx.cpu().numpy(), ri)
+            ref = O.route_scored_backward(stored, ri, d.cpu().numpy(), score="sigmoid")
+            tol = 192 * U + (2.0 ** -8 if dtype == "bf16" else 0) * np.abs(ref)
+            assert (np.abs(g[1:-1].float().cpu().numpy().reshape(T, E) - ref) <= tol).all()
+            assert g[0] == 5.0 and g[-1] == 5.0
