@@ -25,6 +25,8 @@ namespace {
 constexpr float NEG_INF = -__builtin_inff();
 constexpr int RS_WAVES = 4;
 constexpr int RS_MAX_E = 1024;
+// Eight waves a SIMD where the logits leave the registers for it.
+#define RS_OCCUPANCY(items) __attribute__((amdgpu_waves_per_eu((items) <= 8 ? 8 : 1)))
 
 struct ScoredArgs {
   const void* logits;
@@ -36,16 +38,20 @@ struct ScoredArgs {
   float scale;
 };
 
-// The largest x over the 64 lanes, in every lane.
+// The largest x over the 64 lanes, uniform: DPP row shifts gather each row's maximum in its last
+// lane, the broadcasts of lanes 15 and 31 carry it over the rows to lane 63.
 __device__ __forceinline__ float wave_max(float x) {
-  x = fmaxf(x, __int_as_float(dpp_mov<DPP_XOR1>(__float_as_int(x))));
-  x = fmaxf(x, __int_as_float(dpp_mov<DPP_XOR2>(__float_as_int(x))));
-  x = fmaxf(x, __int_as_float(dpp_mov<DPP_HALF_MIRROR>(__float_as_int(x))));
-  x = fmaxf(x, __int_as_float(dpp_mov<DPP_MIRROR>(__float_as_int(x))));
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  auto step = [&](auto ctrl) {
+    constexpr int C = decltype(ctrl)::value;
+    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), C, 0xF, 0xF, false)));
+  };
+  step(std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8
+  step(std::integral_constant<int, 0x112>{});
+  step(std::integral_constant<int, 0x114>{});
+  step(std::integral_constant<int, 0x118>{});
+  step(std::integral_constant<int, 0x142>{});  // row_bcast 15, 31
+  step(std::integral_constant<int, 0x143>{});
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
 // LDS written by some lanes of this wave is read by others after this.
@@ -55,125 +61,187 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Logit `e` of a row, masked (NaN, -inf, the type's lowest value) as -inf, +inf as the largest
-// fp32.
-__device__ __forceinline__ float read_logit(const void* row, int e, int bf16) {
-  const float x = bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(row)[e]) : static_cast<const float*>(row)[e];
+// A logit, masked (NaN, -inf, the type's lowest value) as -inf, +inf as the largest fp32.
+__device__ __forceinline__ float unmask(float x, int bf16) {
   const float lowest = bf16 ? -3.38953139e38f : -3.40282347e38f;
   return x > lowest ? fminf(x, 3.40282347e38f) : NEG_INF;
+}
+
+__device__ __forceinline__ float read_logit(const void* row, int e, int bf16) {
+  return unmask(bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(row)[e]) : static_cast<const float*>(row)[e], bf16);
 }
 
 __device__ __forceinline__ const void* logit_row(const ScoredArgs& a, int t) {
   return static_cast<const char*>(a.logits) + (size_t)t * a.E * (a.bf16 ? 2 : 4);
 }
 
-__device__ __forceinline__ double exp_f(double x) { return exp(x); }
-__device__ __forceinline__ float exp_f(float x) { return __expf(x); }
-
-// The picks of one token in arithmetic F (float: with `close` set where the order of two
-// choices is within their error; double: final). Lane k < K gets the expert of pick k, -1 where
-// no expert was left. l: this lane's logits.
-template <typename F, int ITEMS>
-__device__ __forceinline__ int choose(const ScoredArgs& a, const float (&l)[ITEMS], const float (&bias)[ITEMS],
-                                      float top, F total, int lane, bool& close) {
-  constexpr bool FAST = sizeof(F) == 4;
-  const F ninf = (F)NEG_INF;
-  const int g = lane >> a.lp, p = 1 << a.lp, sub = lane & (p - 1);
-  const bool sums = a.G > 1 && a.group_top == 2;
-  const bool scores = a.bias || sums;
-  F s[ITEMS], c[ITEMS];
+// The fp32 choices of one lane's experts, -inf where masked. top, total: the softmax's largest
+// logit and sum. (The branches are uniform and outside the loops: each loop is straight code.)
+template <int ITEMS>
+__device__ __forceinline__ void choices(const ScoredArgs& a, bool scores, const float (&l)[ITEMS],
+                                        const float (&bias)[ITEMS], float top, float total, float (&s)[ITEMS],
+                                        float (&c)[ITEMS]) {
+  if (!scores) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) s[i] = 0.f;
+  } else if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+  } else {
+    const float inv = 1.0f / total;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) s[i] = __expf(l[i] - top) * inv;
+  }
+  const bool with_bias = a.bias != nullptr;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    s[i] = (F)0;
-    if (scores) {
-      if (a.sigmoid)
-        s[i] = (F)1 / ((F)1 + exp_f(-(F)l[i]));
-      else
-        s[i] = exp_f((F)l[i] - (F)top) / total;
-    }
-    c[i] = a.bias ? s[i] + (F)bias[i] : (F)l[i];
-    if (!(l[i] > NEG_INF && bias[i] > NEG_INF)) c[i] = ninf;
+    c[i] = with_bias ? s[i] + bias[i] : l[i];
+    if (!(l[i] > NEG_INF && bias[i] > NEG_INF)) c[i] = NEG_INF;
   }
-  // How far apart two choices are surely ordered alike in fp32 and exactly. exp errs by
-  // (2 |x| + 2) 2^-24 of its value. Sigmoid: s (1 - s) |x| <= 0.23, so s errs by less than 1.5 *
-  // 2^-22, and rounding c by 2^-24 |c|; twice that is below 2^-20 (1 + |c|). Softmax: the sum
-  // over up to 1024 experts adds at most 2^-18.2, relative to the largest score. Both get a
-  // factor of two on top.
-  F tol = 0;
-  if (FAST && scores) {
-    float big = 0.f;
-    if (a.bias) {
+}
+
+// The fp64 score of a logit.
+__device__ __forceinline__ double exact_score(const ScoredArgs& a, float l, float top, double total) {
+  return a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / total;
+}
+
+// The softmax's sum in fp64.
+template <int ITEMS>
+__device__ __forceinline__ double exact_total(const float (&l)[ITEMS], float top) {
+  double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-        if (c[i] > ninf) big = fmaxf(big, __builtin_fabsf((float)c[i]));
-      big = wave_max(big);
-    }
-    tol = a.sigmoid ? (F)0x1p-19 * ((F)1 + big) : (F)0x1p-16 / total + (F)0x1p-20 * big;
+  for (int i = 0; i < ITEMS; ++i) sum += exp((double)l[i] - (double)top);
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  return sum;
+}
+
+// A step of a butterfly over neighbouring lanes: xor with D for D < 4, else with the mirror image within 2 D
+// lanes, which pairs the same groups once the smaller steps are done.
+template <int D, typename F>
+__device__ __forceinline__ F pair_lane(F v) {
+  constexpr int C = D == 1 ? DPP_XOR1 : D == 2 ? DPP_XOR2 : D == 4 ? DPP_HALF_MIRROR : DPP_MIRROR;
+  if constexpr (D >= 16) {
+    return __shfl_xor(v, D, 64);
+  } else if constexpr (sizeof(F) == 4) {
+    return __int_as_float(dpp_mov<C>(__float_as_int(v)));
+  } else {
+    const int lo = dpp_mov<C>(__double2loint(v)), hi = dpp_mov<C>(__double2hiint(v));
+    return __hiloint2double(hi, lo);
   }
-  bool out = false;  // this lane's group is limited away
-  if (a.G > 1) {
-    F m1 = ninf, m2 = ninf;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const F u = c[i] > ninf ? (sums && !a.bias ? s[i] : c[i]) : ninf;
-      m2 = u > m1 ? m1 : (u > m2 ? u : m2);
-      m1 = u > m1 ? u : m1;
-    }
-    for (int d = 1; d < p; d <<= 1) {
-      const F o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
-      const F lo = o1 > m1 ? m1 : o1;
-      const F hi2 = o2 > m2 ? o2 : m2;
-      m2 = lo > hi2 ? lo : hi2;
-      m1 = o1 > m1 ? o1 : m1;
-    }
-    F score = m1;
-    if (sums && m2 > ninf) score = m1 + m2;
-    int rank = 0;
+}
+
+__device__ __forceinline__ float lane_value(float v, int j) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
+}
+__device__ __forceinline__ double lane_value(double v, int j) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), j), __builtin_amdgcn_readlane(__double2loint(v), j));
+}
+
+// The two largest choices of a lane's experts, m1 >= m2.
+template <typename F>
+__device__ __forceinline__ void top_two(F u, F& m1, F& m2) {
+  m2 = u > m1 ? m1 : (u > m2 ? u : m2);
+  m1 = u > m1 ? u : m1;
+}
+
+// Whether this lane's group stays, from its lanes' two largest choices. tol > 0: `close` is set where
+// a kept and a dropped group's scores differ by no more than 2 tol.
+template <typename F>
+__device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, F tol, F m1, F m2, bool& close) {
+  const F ninf = (F)NEG_INF;
+  const int g = lane >> a.lp;
+  auto merge = [&](F o1, F o2) {
+    const F lo = o1 > m1 ? m1 : o1;
+    const F hi = o2 > m2 ? o2 : m2;
+    m2 = lo > hi ? lo : hi;
+    m1 = o1 > m1 ? o1 : m1;
+  };
+  if (a.lp >= 1) merge(pair_lane<1>(m1), pair_lane<1>(m2));
+  if (a.lp >= 2) merge(pair_lane<2>(m1), pair_lane<2>(m2));
+  if (a.lp >= 3) merge(pair_lane<4>(m1), pair_lane<4>(m2));
+  if (a.lp >= 4) merge(pair_lane<8>(m1), pair_lane<8>(m2));
+  if (a.lp >= 5) merge(pair_lane<16>(m1), pair_lane<16>(m2));
+  const F score = a.group_top == 2 && m2 > ninf ? m1 + m2 : m1;
+  int rank = 0;
+  bool near = false;
+  for (int j = 0; j < a.G; ++j) {
+    const F o = lane_value(score, j << a.lp);
+    rank += (o > score || (o == score && j < g)) ? 1 : 0;
+    near |= j != g && o - score <= 2 * tol && score - o <= 2 * tol;
+  }
+  const bool kept = g < a.G && rank < a.topk_groups;
+  if (tol > 0 && __ballot(near && g < a.G)) {  // only a pair across the border matters
     for (int j = 0; j < a.G; ++j) {
-      const F o = __shfl(score, j << a.lp, 64);
-      rank += (o > score || (o == score && j < g)) ? 1 : 0;
-      if (FAST && scores && j != g && o > ninf && score > ninf && o - score <= 2 * tol && score - o <= 2 * tol)
-        close = true;
+      const F o = lane_value(score, j << a.lp);
+      const bool o_kept = __builtin_amdgcn_readlane((int)kept, j << a.lp);
+      close |= kept != o_kept && g < a.G && o - score <= 2 * tol && score - o <= 2 * tol;
     }
-    out = g >= a.G || rank >= a.topk_groups;
+  }
+  return kept;
+}
+
+// The plain way, in fp64: K rounds of a wave-wide arg-max over the logits in row (LDS). Lane k < K
+// gets pick k, or -1. Few tokens come here: it is kept small, with rolled loops
+// that compute a choice anew each time, so that its registers do not cost the common path waves.
+__device__ __forceinline__ int choose_exact(ScoredArgs a, const float* row, float top) {
+  const int lane = threadIdx.x & 63;
+  const int g = lane >> a.lp, p = 1 << a.lp, sub = lane & (p - 1);
+  const double ninf = (double)NEG_INF;
+  const int items = g < a.G ? (a.S - sub + p - 1) >> a.lp : 0;
+  double total = 0.0;
+  if (!a.sigmoid) {
+#pragma unroll 1
+    for (int i = 0; i < items; ++i) total += exp((double)row[g * a.S + (i << a.lp) + sub] - (double)top);
+    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d, 64);
+  }
+  // want_s: the score where a choice is a bare logit
+  auto choice = [&](int i, bool want_s) {
+    const int e = g * a.S + (i << a.lp) + sub;
+    const float l = row[e];
+    const float b = a.bias ? a.bias[e] : 0.f;
+    if (!(l > NEG_INF && b > NEG_INF)) return ninf;
+    if (a.bias || want_s) return exact_score(a, l, top, total) + (double)b;
+    return (double)l;
+  };
+  bool kept = true;
+  if (a.G > 1) {
+    double m1 = ninf, m2 = ninf;
+#pragma unroll 1
+    for (int i = 0; i < items; ++i) top_two(choice(i, a.group_top == 2), m1, m2);
+    bool close = false;
+    kept = group_kept<double>(a, lane, 0.0, m1, m2, close);
   }
   uint32_t taken = 0;
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
-    if (out || !(c[i] > ninf)) taken |= 1u << i;
   int my_e = -1;
-  F last = ninf;
-  // with a bias, in fp32 one round more: the best expert not picked, against the last pick
-  const bool near = FAST && a.bias;
-  const int rounds = near ? a.K + 1 : a.K;
-  for (int k = 0; k < rounds; ++k) {
-    F bv = ninf;
+#pragma unroll 1
+  for (int k = 0; k < a.K; ++k) {
+    double bv = ninf;
     int bi = -1;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-      if (!((taken >> i) & 1) && c[i] > bv) {  // a lane's experts rise with i: ties keep the lower
-        bv = c[i];
-        bi = i;
+    if (kept) {
+#pragma unroll 1
+      for (int i = 0; i < items; ++i) {
+        if ((taken >> i) & 1) continue;
+        const double c = choice(i, false);
+        if (c > bv) {  // a lane's experts rise with i: ties keep the lower
+          bv = c;
+          bi = i;
+        }
       }
+    }
     const int mine = bi < 0 ? 0x7fffffff : g * a.S + (bi << a.lp) + sub;
     int be = mine;
-    if constexpr (FAST) {
-      wave_best(bv, be);
-    } else {
-      for (int d = 1; d < 64; d <<= 1) {
-        const F ov = __shfl_xor(bv, d, 64);
-        const int oe = __shfl_xor(be, d, 64);
-        if (ov > bv || (ov == bv && oe < be)) {
-          bv = ov;
-          be = oe;
-        }
+#pragma unroll 1
+    for (int d = 1; d < 64; d <<= 1) {
+      const double ov = __shfl_xor(bv, d, 64);
+      const int oe = __shfl_xor(be, d, 64);
+      if (ov > bv || (ov == bv && oe < be)) {
+        bv = ov;
+        be = oe;
       }
     }
     if (be == 0x7fffffff) break;  // no expert left (the same in every lane)
     if (mine == be) taken |= 1u << bi;
-    if (near && k > 0 && last - bv <= tol) close = true;
-    last = bv;
-    if (lane == k && k < a.K) my_e = be;
+    if (lane == k) my_e = be;
   }
   return my_e;
 }
@@ -192,25 +260,55 @@ __device__ __forceinline__ float pick_share(float l, bool on, bool sigmoid) {
   return on ? s / sum : 0.f;
 }
 
+// One wave per token:
+//  1. the choices in fp32, group limits;
+//  2. a threshold: the K-th largest of the lanes' own maxima, at most the K-th largest choice,
+//     found by K rounds of a wave maximum of one value per lane;
+//  3. the few choices from the threshold up (less the error bound) go to LDS and come back one per lane: the
+//     candidates, usually K to 2 K of them;
+//  4. a candidate's rank is the number of candidates before it. Where two of them lie within the error bound,
+//     each lane computes its own candidate's choice in fp64 and the ranks are taken from those.
+// Where the scores of a kept and a dropped group lie within the bound, the group scores are taken in fp64
+// too. A rank below K is a pick, written by the lane that holds it. Tokens with more than 64
+// candidates (many equal choices) take the plain way in fp64.
 template <int ITEMS>
-__global__ __launch_bounds__(64 * RS_WAVES) void route_scored_kernel(ScoredArgs a, int* __restrict__ topk_idx,
+__global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_scored_kernel(ScoredArgs a, int* __restrict__ topk_idx,
                                                                      float* __restrict__ topk_w) {
   __shared__ float rows[RS_WAVES][RS_MAX_E];
+  __shared__ float2 cand[RS_WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t = blockIdx.x * RS_WAVES + wave;
   if (t >= a.T) return;
   const void* row = logit_row(a, t);
-  const int g = lane >> a.lp, p = 1 << a.lp, sub = lane & (p - 1);
+  const int g = lane >> a.lp, sub = lane & ((1 << a.lp) - 1);
   float* mine = rows[wave];
   float l[ITEMS], bias[ITEMS];
+  int at[ITEMS];
+  bool in[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int r = (i << a.lp) + sub;
-    const bool in = g < a.G && r < a.S;
-    const int e = in ? g * a.S + r : 0;
-    bias[i] = a.bias ? a.bias[e] : 0.f;
-    l[i] = in ? read_logit(row, e, a.bf16) : NEG_INF;
-    if (in) mine[e] = l[i];
+    in[i] = g < a.G && r < a.S;
+    at[i] = in[i] ? g * a.S + r : 0;  // lanes without an expert read expert 0: all loads go out together
+  }
+  if (a.bf16) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) l[i] = bf16_bits_to_f32(static_cast<const uint16_t*>(row)[at[i]]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) l[i] = static_cast<const float*>(row)[at[i]];
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) bias[i] = a.bias[at[i]];
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) bias[i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    l[i] = in[i] ? unmask(l[i], a.bf16) : NEG_INF;
+    if (in[i]) mine[at[i]] = l[i];
   }
   float top = 0.f, total = 1.f;
   if (!a.sigmoid && (a.bias || a.G > 1 || !a.renorm)) {
@@ -224,30 +322,114 @@ __global__ __launch_bounds__(64 * RS_WAVES) void route_scored_kernel(ScoredArgs 
     for (int i = 0; i < ITEMS; ++i) z += __expf(l[i] - top);
     total = wave_sum(z);
   }
-  bool close = false;
-  int my_e = choose<float, ITEMS>(a, l, bias, top, total, lane, close);
-  if (__ballot(close)) {
-    double sum = 1.0;
-    if (!a.sigmoid) {
-      sum = 0.0;
+  const bool scores = a.bias || (a.G > 1 && a.group_top == 2);
+  float s[ITEMS], c[ITEMS];
+  choices<ITEMS>(a, scores, l, bias, top, total, s, c);
+  // How far apart two choices are surely ordered alike in fp32 and exactly. exp errs by
+  // (2 |x| + 2) 2^-24 of its value. Sigmoid: s (1 - s) |x| <= 0.23, so s errs by less than 1.5 *
+  // 2^-22, and rounding c by 2^-24 |c|; twice that is below 2^-20 (1 + |c|). Softmax: the sum
+  // over up to 1024 experts adds at most 2^-18.2, relative to the largest score, 1 / total. Both
+  // get a factor of two on top. Without scores the choices are the logits: exact.
+  float tol = 0.f;
+  if (scores) {
+    float big = 0.f;
+    if (a.bias) {
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) sum += exp((double)l[i] - (double)top);
-      for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+      for (int i = 0; i < ITEMS; ++i)
+        if (c[i] > NEG_INF) big = fmaxf(big, __builtin_fabsf(c[i]));
+      big = wave_max(big);
     }
-    my_e = choose<double, ITEMS>(a, l, bias, top, sum, lane, close);
+    tol = a.sigmoid ? 0x1p-19f * (1.0f + big) : 0x1p-16f / total + 0x1p-20f * big;
   }
+  bool close = false;
+  if (a.G > 1) {
+    const bool use_s = a.group_top == 2 && !a.bias;
+    float m1 = NEG_INF, m2 = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) top_two(c[i] > NEG_INF ? (use_s ? s[i] : c[i]) : NEG_INF, m1, m2);
+    bool kept = group_kept<float>(a, lane, tol, m1, m2, close);
+    if (__ballot(close)) {
+      const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
+      double d1 = (double)NEG_INF, d2 = d1;
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+        if (c[i] > NEG_INF) top_two(exact_score(a, l[i], top, sum) + (double)bias[i], d1, d2);
+      kept = group_kept<double>(a, lane, 0.0, d1, d2, close);
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (!kept) c[i] = NEG_INF;
+  }
+  bool plain = !(tol < 1e30f);  // an infinite or huge bias
+  const float gap = a.bias ? tol : 0.f;
+
+  float own = NEG_INF;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) own = fmaxf(own, c[i]);
+  float bar = NEG_INF;
+  for (int k = 0; k < a.K; ++k) {
+    bar = wave_max(own);
+    own = own == bar ? NEG_INF : own;
+  }
+  bar -= gap;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const bool is = c[i] >= bar && c[i] > NEG_INF;
+    const uint64_t m = __ballot(is);
+    if (m) {
+      const int place = n + popc_below(m);
+      if (is && place < 64) cand[wave][place] = make_float2(c[i], __int_as_float(at[i]));
+      n += __popcll(m);
+    }
+  }
+  plain = plain || n > 64;
   wave_sync();
-  const bool on = my_e >= 0;
-  const float lp = on ? mine[my_e] : NEG_INF;
-  float w;
-  if (a.renorm) {
-    w = pick_share(lp, on, a.sigmoid);
+  int my_e = -1, rank = 64;
+  if (!plain) {
+    float v = NEG_INF;
+    int e = 0x7fffffff;
+    if (lane < n) {
+      const float2 x = cand[wave][lane];
+      v = x.x;
+      e = __float_as_int(x.y);
+    }
+    auto ranks = [&](auto x) {
+      bool near = false;
+      rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const auto o = lane_value(x, j);
+        const int oe = __builtin_amdgcn_readlane(e, j);
+        rank += (o > x || (o == x && oe < e)) ? 1 : 0;
+        if constexpr (sizeof(x) == 4) near |= oe != e && __builtin_fabsf(o - x) <= gap;
+      }
+      return near;
+    };
+    const bool near = ranks(v);
+    if (a.bias && __ballot(near && lane < n)) {
+      const float lv = lane < n ? mine[e] : 0.f;
+      const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
+      const double x = lane < n ? exact_score(a, lv, top, sum) + (double)a.bias[e] : (double)NEG_INF;
+      (void)ranks(x);
+    }
+    const bool on = lane < n && rank < a.K;
+    my_e = on ? e : -1;
+    // positions that no candidate takes: -1 from the lanes above the candidates
+    if (!on) rank = lane >= n && lane < a.K ? lane : 64;
   } else {
-    w = !on ? 0.f : a.sigmoid ? sigmoid_f32(lp) : expf(lp - top) / total;
+    my_e = choose_exact(a, mine, top);
+    rank = lane;
   }
-  if (lane < a.K) {
-    topk_idx[(size_t)t * a.K + lane] = my_e;
-    topk_w[(size_t)t * a.K + lane] = w * a.scale;
+  const bool on = my_e >= 0;
+  const float lv = on ? mine[my_e] : NEG_INF;
+  float w;
+  if (a.renorm)
+    w = pick_share(lv, on, a.sigmoid);
+  else
+    w = !on ? 0.f : a.sigmoid ? sigmoid_f32(lv) : expf(lv - top) / total;
+  if (rank < a.K) {
+    topk_idx[(size_t)t * a.K + rank] = my_e;
+    topk_w[(size_t)t * a.K + rank] = w * a.scale;
   }
 }
 
