@@ -37,10 +37,11 @@ constexpr int M4_OUT = (int)0x80000000u;  // an offset past every range: loads z
 constexpr int M4_A_BYTES = M4_BM * M4_BK / 2;
 constexpr int M4_B_BYTES = M4_BN * M4_BK / 2;
 constexpr int M4_LD = M4_A_BYTES / (1024 * 8);   // wave loads per stage, each operand
-constexpr int M4_SF_A = M4_A_BYTES + M4_B_BYTES;  // activation scales [256][8]
-constexpr int M4_SF_B = M4_SF_A + M4_BM * 8;      // weight scales [8][BN per matrix] per matrix
+constexpr int M4_SF_B = M4_A_BYTES + M4_B_BYTES;  // weight scales [8][BN per matrix] per matrix
 constexpr int M4_STAGE = M4_SF_B + M4_BN * 8;
-constexpr int M4_LDS = M4_NS * M4_STAGE + (M4_MAX_E + 1 + 16) * 4;
+constexpr int M4_SF_A = M4_BM * 32;               // activation scales of four stages [256][32]
+constexpr int M4_SCHED = M4_NS * (M4_STAGE + M4_SF_A);
+constexpr int M4_LDS = M4_SCHED + (M4_MAX_E + 1 + 16) * 4;
 static_assert(M4_LDS <= 160 * 1024, "LDS budget");
 
 struct Mx4Args {
@@ -60,7 +61,8 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   constexpr int BN = M4_BN / NB;   // columns per matrix
   constexpr int NT = BN / 64;      // 32-column blocks of a wave per matrix
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  int* tstart = reinterpret_cast<int*>(smem + M4_NS * M4_STAGE);
+  unsigned char* sf_a = smem + M4_NS * M4_STAGE;
+  int* tstart = reinterpret_cast<int*>(smem + M4_SCHED);
   int* wsum = tstart + M4_MAX_E + 1;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -84,8 +86,9 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     ld_row[i] = (wave + 8 * i) * 8 + (lane >> 3);
     ld_chunk[i] = (lane & 7) ^ ((ld_row[i] >> 1) & 7);
   }
-  // Scales: of the rows, dword lane % 2 of row 32 wave + lane / 2; of the columns, LDS [NB][8][BN], bytes
-  // 256 wave .. of the block.
+  // Scales of the columns: LDS [NB][8][BN], bytes 256 wave .. of the block. Scales of the rows: half
+  // lane % 2 of the 32 bytes of row 32 wave + lane / 2, for four stages at once. They lie row by row, a cache
+  // line per row however few bytes are taken, and it is the lines asked for that bound the loads.
   const int sa_row = wave * 32 + (lane >> 1), sa_half = lane & 1;
   const int sb_byte = wave * 256 + lane * 4;
   const int sb_nb = sb_byte / (8 * BN), sb_kb = (sb_byte / BN) & 7, sb_col = sb_byte % BN;
@@ -118,14 +121,14 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
 #pragma unroll
       for (int i = 0; i < M4_LD; ++i)
         d.a_off[i] = (ld_row[i] < d.rows_valid && src[i] >= 0) ? (src[i] / a.a_k) * kb + ld_chunk[i] * 16 : M4_OUT;
-      d.s_off = (sa_row < d.rows_valid && ssrc >= 0) ? (ssrc / a.a_k) * ksf + sa_half * 4 : M4_OUT;
+      d.s_off = (sa_row < d.rows_valid && ssrc >= 0) ? (ssrc / a.a_k) * ksf + sa_half * 16 : M4_OUT;
     } else {
       d.rA = make_rsrc(a.A + (size_t)d.row0 * kb, (uint32_t)d.rows_valid * (uint32_t)kb);
       d.rS = make_rsrc(a.A_sf + (size_t)d.row0 * ksf, (uint32_t)d.rows_valid * (uint32_t)ksf);
 #pragma unroll
       for (int i = 0; i < M4_LD; ++i)
         d.a_off[i] = ld_row[i] < d.rows_valid ? ld_row[i] * kb + ld_chunk[i] * 16 : M4_OUT;
-      d.s_off = sa_row < d.rows_valid ? sa_row * ksf + sa_half * 4 : M4_OUT;
+      d.s_off = sa_row < d.rows_valid ? sa_row * ksf + sa_half * 16 : M4_OUT;
     }
     d.nmt = __builtin_amdgcn_readfirstlane((wm * 32 < d.rows_valid) + (128 + wm * 32 < d.rows_valid));
     const size_t wbase = ((size_t)d.e * N + d.n0) * kb;
@@ -147,11 +150,16 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       lds_dma16(second ? d.rB1 : d.rB0, so + M4_A_BYTES + (wave + 8 * i) * 1024,
                 cut && ld_chunk[i] >= 4 ? M4_OUT : c * kb + ld_chunk[i] * 16, kt * (M4_BK / 2));
     }
-    lds_dma4(d.rS, so + M4_SF_A + wave * 256, cut && sa_half ? M4_OUT : d.s_off, kt * 8);
     const int planes = min(8, ksf - 8 * kt);
     const uint8_t* sfb = (GATED && sb_nb) ? a.B1_sf : a.B0_sf;
     lds_dma4(make_rsrc(sfb + ((size_t)d.e * ksf + 8 * (size_t)kt) * N, (uint32_t)N * (uint32_t)planes),
              so + M4_SF_B + wave * 256, sb_kb < planes && d.n0 + sb_col < N ? sb_kb * N + d.n0 + sb_col : M4_OUT, 0);
+  };
+
+  // The row scales of stages 4q..4q+3, into half `ab`; bytes past the last row's read as zero, so the whole
+  // offset is in the checked part.
+  auto issue_sf = [&](const Tile& d, int q, int ab) __attribute__((always_inline)) {
+    lds_dma16(d.rS, lds0 + M4_NS * M4_STAGE + ab * M4_SF_A + wave * 1024, d.s_off + q * 32, 0);
   };
 
   // Fragments: row (column) block + lane % 32, chunk 4G + kk.
@@ -162,11 +170,12 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) f_off[kk] = ((4 * g2 + kk) ^ sw) << 4;
 
-  int buf = 0;
+  int buf = 0, ab = 0;
   Tile cur;
   if (slot < total) {
     cur = decode(slot);
-    issue(cur, 0, 0);
+    issue_sf(cur, 0, ab);
+    issue(cur, 0, buf);
   }
   for (int t = slot; t < total; t += G) {
     f32x16_t acc[NB][2][NT];
@@ -184,13 +193,19 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       for (int kt = 0; kt < nk; ++kt) {
         // stage kt has landed for every wave, and every wave is done with the other buffer
         wait_barrier<0>();
+        if ((kt & 3) == 0) {
+          if (kt > 0) ab ^= 1;
+          if (kt + 4 < nk) issue_sf(cur, kt / 4 + 1, ab ^ 1);
+        }
         if (kt + 1 < nk) issue(cur, kt + 1, buf ^ 1);
         if constexpr (MTV > 0) {
           const unsigned char* st = smem + buf * M4_STAGE;
           int sa[MTV];
 #pragma unroll
-          for (int mt = 0; mt < MTV; ++mt)
-            sa[mt] = *reinterpret_cast<const int*>(st + M4_SF_A + (mt * 128 + ar) * 8 + 4 * g2);
+          for (int mt = 0; mt < MTV; ++mt) {
+            sa[mt] = *reinterpret_cast<const int*>(sf_a + ab * M4_SF_A + (mt * 128 + ar) * 32 + (kt & 3) * 8 + 4 * g2);
+            if (half && kt == nk - 1 && g2) sa[mt] = 0;  // the absent blocks' bytes are another row's
+          }
           auto step = [&](auto kk_) __attribute__((always_inline)) {
             constexpr int kk = decltype(kk_)::value;
             const i32x4_t z = {0, 0, 0, 0};
@@ -231,6 +246,8 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     // passed the last barrier.
     if (t + G < total) {
       cur = decode(t + G);
+      ab ^= 1;
+      issue_sf(cur, 0, ab);
       issue(cur, 0, buf);
     }
 
@@ -277,6 +294,198 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   }
 }
 
+// ---- few rows per expert --------------------------------------------------------------
+//
+// With a handful of rows per expert the weights are read once and hardly reused: what counts is to
+// have many of their bytes in flight. A wave takes 16 columns of one matrix and streams them past up to
+// 16 RG rows straight into registers, no LDS, with the weights as the first operand of
+// v_mfma_scale_f32_16x16x128_f8f6f4 (lane l: column l % 16, block G = l / 16 of the step's four) and the rows as
+// the second. In a step of 512 a lane takes the 64 bytes at 64 G of its column, two whole lines
+// per column and step, and the next step's loads are out before this one's products. A block
+// of eight waves takes 32 columns of gate and of up, each split in two along the reduction, and adds and rounds
+// through LDS (one block of the format is 32 columns), or 128 columns of down. Blocks walk the
+// experts that have rows.
+
+constexpr int S4_THREADS = 512;
+
+template <int RG>
+struct S4Step {
+  i32x4_t w[4], x[RG][4];
+  int ws[4], xs[RG];
+};
+
+template <bool GATED, int RG>
+__global__ __launch_bounds__(S4_THREADS) void ffn_mxfp4_stream_kernel(Mx4Args a) {
+  constexpr int BN = GATED ? 32 : 128;  // columns of a block
+  __shared__ float part[GATED ? 8 : 1][GATED ? RG : 1][16][17];  // [wave][row group][row][column]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = a.N, kb = a.Kd / 2, ksf = a.Kd / 32;
+  const int ncb = N / BN;
+  const int idx = xcd_slot(blockIdx.x, gridDim.x);
+  const int cb = idx % ncb;
+  int left = idx / ncb, e = -1;
+  for (int base = 0; base < a.E; base += 64) {  // the left-th expert that has rows
+    const int i = base + lane;
+    const uint64_t m = __ballot(i < a.E && a.cu[min(i, a.E - 1) + 1] > a.cu[min(i, a.E - 1)]);
+    const int n = __popcll(m);
+    if (left < n) {
+      const uint64_t hit = __ballot(((m >> lane) & 1) && popc_below(m) == left);
+      e = base + __builtin_ctzll(hit);
+      break;
+    }
+    left -= n;
+  }
+  if (e < 0) return;
+  const int gbeg = __builtin_amdgcn_readfirstlane(a.cu[e]);
+  const int rows = __builtin_amdgcn_readfirstlane(a.cu[e + 1]) - gbeg;
+
+  const int c16 = lane & 15, G = lane >> 4;
+  const int nb = GATED ? (wave >> 1) & 1 : 0;
+  const int n0 = cb * BN + (GATED ? (wave & 1) * 16 : wave * 16);
+  const uint8_t* wp = (nb ? a.B1 : a.B0) + ((size_t)e * N + n0 + c16) * kb + G * 64;
+  const uint8_t* wsp = (nb ? a.B1_sf : a.B0_sf) + ((size_t)e * ksf + 4 * G) * N + n0 + c16;
+  const int steps = (kb + 255) / 256;
+  const int first = GATED && wave >= 4 ? (steps + 1) / 2 : 0;
+  const int last = GATED && wave < 4 ? (steps + 1) / 2 : steps;
+
+  for (int r0 = 0; r0 < rows; r0 += 16 * RG) {
+    const uint8_t *xp[RG], *xsp[RG];
+    int nrg = 0;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      // rows past the last read it again; their results are not stored
+      int r = gbeg + min(r0 + 16 * g + c16, rows - 1);
+      if (GATED && a.row_src) {
+        const int src = a.row_src[r];
+        r = src < 0 ? 0 : min(src / a.a_k, a.a_rows - 1);
+      }
+      xp[g] = a.A + (size_t)r * kb + G * 64;
+      xsp[g] = a.A_sf + (size_t)r * ksf + 4 * G;
+      nrg += r0 + 16 * g < rows;
+    }
+    f32x4_t acc[RG];
+#pragma unroll
+    for (int g = 0; g < RG; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // Step `it` of this lane; past the end of the reduction (a last step that is not whole) zeros.
+    auto load = [&](S4Step<RG>& d, int it) __attribute__((always_inline)) {
+      const bool in = it * 256 + G * 64 < kb;
+      const int o = in ? it * 256 : 0, os = in ? it * 16 : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) d.w[q] = *reinterpret_cast<const i32x4_t*>(wp + (in ? o : -G * 64) + 16 * q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) d.ws[q] = wsp[(ptrdiff_t)(in ? os + q : -4 * G) * N];
+#pragma unroll
+      for (int g = 0; g < RG; ++g)
+        if (g < nrg) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) d.x[g][q] = *reinterpret_cast<const i32x4_t*>(xp[g] + (in ? o : -G * 64) + 16 * q);
+          d.xs[g] = *reinterpret_cast<const int*>(xsp[g] + (in ? os : -4 * G));
+        }
+      if (!in) {
+        const i32x4_t z = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          d.w[q] = z;
+          d.ws[q] = 0;
+        }
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) d.x[g][q] = z;
+          d.xs[g] = 0;
+        }
+      }
+    };
+    auto mul = [&](const S4Step<RG>& d) __attribute__((always_inline)) {
+      const i32x4_t z = {0, 0, 0, 0};
+      auto one = [&](auto q_) __attribute__((always_inline)) {
+        constexpr int q = decltype(q_)::value;
+        const i32x8_t wf = __builtin_shufflevector(d.w[q], z, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int g = 0; g < RG; ++g)
+          if (g < nrg) {
+            const i32x8_t xf = __builtin_shufflevector(d.x[g][q], z, 0, 1, 2, 3, 4, 5, 6, 7);
+            acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[g], 4, 4, 0, d.ws[q], q, d.xs[g]);
+          }
+      };
+      one(std::integral_constant<int, 0>{});
+      one(std::integral_constant<int, 1>{});
+      one(std::integral_constant<int, 2>{});
+      one(std::integral_constant<int, 3>{});
+    };
+    S4Step<RG> s0, s1;
+    if (first < last) load(s0, first);
+    for (int it = first; it < last; it += 2) {
+      if (it + 1 < last) load(s1, it + 1);
+      mul(s0);
+      if (it + 2 < last) load(s0, it + 2);
+      if (it + 1 < last) mul(s1);
+    }
+
+    // lane l holds row l % 16 of its group, columns 4G..4G+3 of the wave's 16
+    if constexpr (GATED) {
+      __syncthreads();  // the previous row chunk's sums are read
+#pragma unroll
+      for (int g = 0; g < RG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[wave][g][c16][4 * G + i] = acc[g][i];
+      __syncthreads();
+      // wave g rounds row group g: lane = 4 row + quarter of the 32 columns
+      const int r = lane >> 2, j = lane & 3;
+      if (wave < RG && r0 + 16 * wave + r < rows) {
+        const int row = gbeg + r0 + 16 * wave + r;
+        const bool pad = a.row_src && a.row_src[row] < 0;
+        float v[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int hw = j >> 1, c = (j & 1) * 8 + i;
+          const float gate = part[hw][wave][r][c] + part[4 + hw][wave][r][c];
+          const float up = part[2 + hw][wave][r][c] + part[6 + hw][wave][r][c];
+          v[i] = pad ? 0.f : silu_f32(gate) * up;
+          m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        }
+        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
+        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
+        const uint32_t byte = mx_scale_byte(m);
+        *reinterpret_cast<uint32_t*>(a.h_q + (size_t)row * (N / 2) + cb * 16 + 4 * j) = mx_pack8(v, byte);
+        if (j == 0) a.h_sf[(size_t)row * (N / 32) + cb] = (uint8_t)byte;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+        const int r = r0 + 16 * g + c16;
+        if (r < rows)
+          *reinterpret_cast<uint2*>(a.y + (size_t)(gbeg + r) * N + n0 + 4 * G) =
+              make_uint2(pack_bf16x2(acc[g][0], acc[g][1]), pack_bf16x2(acc[g][2], acc[g][3]));
+      }
+    }
+  }
+}
+
+template <bool GATED>
+moe_status_t launch_stream(const Mx4Args& a, int M, hipStream_t s) {
+  const int slots = M < a.E ? M : a.E;  // at most so many experts have rows
+  const int64_t grid = (int64_t)slots * (a.N / (GATED ? 32 : 128));
+  if (M <= 8 * slots)
+    ffn_mxfp4_stream_kernel<GATED, 1><<<(unsigned)grid, S4_THREADS, 0, s>>>(a);
+  else
+    ffn_mxfp4_stream_kernel<GATED, 2><<<(unsigned)grid, S4_THREADS, 0, s>>>(a);
+  return launch_status();
+}
+
+// Whether the streaming kernel takes M rows over E experts and N columns in tiles of bn. It does
+// where the tiles could not fill the chip: up to `slots` experts have rows, each with N / bn
+// tiles. On 256 CUs, H 7168, Hp 2048, gate/up: one token of 8 experts (128 tiles) 28 us against
+// the tiles' 47, two tokens (256) 54 against 53, eight (672) 161 against 142; H 2048, Hp 1024: one
+// token of 6 experts 7.9 against 15.7, four (168) 15.1 against 17.7, sixteen (424) 39 against 36. More than
+// 16 rows per expert would stream the weights more than once.
+bool streams(int M, int E, int N, int bn) {
+  const int slots = M < E ? M : E;
+  return M <= 16 * slots && (int64_t)slots * ((N + bn - 1) / bn) <= device_cu_count();
+}
+
 template <bool GATED>
 moe_status_t launch_tiles(const Mx4Args& a, hipStream_t s) {
   static std::atomic<unsigned char> lds_set[MOE_MAX_DEVICES];
@@ -294,6 +503,7 @@ moe_status_t launch_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, c
                                       uint8_t* h_sf, hipStream_t s) {
   if (M == 0) return MOE_OK;
   const Mx4Args a{x_q, x_sf, row_src, K, T, cu, E, H, Hp, wg, sg, wu, su, h_q, h_sf, nullptr};
+  if (streams(M, E, Hp, M4_BN / 2) && (!row_src || T > 0)) return launch_stream<true>(a, M, s);
   return launch_tiles<true>(a, s);
 }
 
@@ -302,6 +512,7 @@ moe_status_t launch_ffn_down_mxfp4(const uint8_t* h_q, const uint8_t* h_sf, cons
   if (M == 0) return MOE_OK;
   const Mx4Args a{h_q, h_sf, nullptr, 1, 0, cu, E, Hp, H, wd, sd, nullptr, nullptr, nullptr, nullptr,
                   static_cast<uint16_t*>(y)};
+  if (streams(M, E, H, M4_BN)) return launch_stream<false>(a, M, s);
   return launch_tiles<false>(a, s);
 }
 
