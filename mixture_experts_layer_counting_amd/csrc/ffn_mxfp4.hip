@@ -79,12 +79,15 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   const uint32_t lds0 = lds_addr(smem);
 
   // Loads of a stage: wave load j = wave + 8 i covers rows (columns) 8j..8j+7, lane -> row 8j + lane/8, slot
-  // lane % 8 of which holds chunk slot ^ (row/2 mod 8). Chunks 4..7 are absent in a half stage.
-  int ld_row[M4_LD], ld_chunk[M4_LD];
+  // lane % 8 of which holds chunk slot ^ (row/2 mod 8), for columns slot ^ (column/NT mod 8): eight neighbouring
+  // lanes of a fragment read, NT columns apart, then hit eight different slots. Chunks 4..7 are
+  // absent in a half stage.
+  int ld_row[M4_LD], ld_chunk[M4_LD], ld_bchunk[M4_LD];
 #pragma unroll
   for (int i = 0; i < M4_LD; ++i) {
     ld_row[i] = (wave + 8 * i) * 8 + (lane >> 3);
     ld_chunk[i] = (lane & 7) ^ ((ld_row[i] >> 1) & 7);
+    ld_bchunk[i] = (lane & 7) ^ ((ld_row[i] / NT) & 7);
   }
   // Scales of the columns: LDS [NB][8][BN], bytes 256 wave .. of the block. Scales of the rows: half
   // lane % 2 of the 32 bytes of row 32 wave + lane / 2, for four stages at once. They lie row by row, a cache
@@ -148,7 +151,7 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       const bool second = GATED && i >= M4_LD / 2;
       const int c = ld_row[i] - (second ? BN : 0);
       lds_dma16(second ? d.rB1 : d.rB0, so + M4_A_BYTES + (wave + 8 * i) * 1024,
-                cut && ld_chunk[i] >= 4 ? M4_OUT : c * kb + ld_chunk[i] * 16, kt * (M4_BK / 2));
+                cut && ld_bchunk[i] >= 4 ? M4_OUT : c * kb + ld_bchunk[i] * 16, kt * (M4_BK / 2));
     }
     const int planes = min(8, ksf - 8 * kt);
     const uint8_t* sfb = (GATED && sb_nb) ? a.B1_sf : a.B0_sf;
@@ -162,13 +165,19 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     lds_dma16(d.rS, lds0 + M4_NS * M4_STAGE + ab * M4_SF_A + wave * 1024, d.s_off + q * 32, 0);
   };
 
-  // Fragments: row (column) block + lane % 32, chunk 4G + kk.
+  // Fragments: chunk 4G + kk of row (block) + l, l = lane % 32. Block nt of a wave's columns takes every NT-th
+  // column, nt + NT l, so that the scale bytes of a lane's NT columns are neighbours and one LDS
+  // read brings them all.
   const int g2 = lane >> 5, l32 = lane & 31;
   const int ar = wm * 32 + l32;
-  const int sw = (l32 >> 1) & 7;  // the same for every 32-row block
-  int f_off[4];
+  const int wcol = wn * (BN / 2) + NT * l32;
+  int fa_off[4], fb_off[4];
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) f_off[kk] = ((4 * g2 + kk) ^ sw) << 4;
+  for (int kk = 0; kk < 4; ++kk) {
+    fa_off[kk] = ar * 128 + (((4 * g2 + kk) ^ ((l32 >> 1) & 7)) << 4);  // the same for every 32-row block
+    fb_off[kk] = M4_A_BYTES + wcol * 128 + (((4 * g2 + kk) ^ (l32 & 7)) << 4);
+  }
+  const int sb_off = M4_SF_B + 4 * g2 * BN + wcol;
 
   int buf = 0, ab = 0;
   Tile cur;
@@ -188,10 +197,58 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[nb][mt][nt][i] = 0.f;
 
+    // The K loop over the first MTV row blocks of this wave. The fragments of a step are read while
+    // the products of the step before run, across the stage barrier too: the last step of a stage
+    // is in registers when the stage is given up.
     auto k_loop = [&](auto mtv) {
       constexpr int MTV = decltype(mtv)::value;
+      constexpr int MR = MTV ? MTV : 1;
+      struct Frag {
+        i32x4_t a[MR], b[NB][NT];
+        int sb[NB];
+      };
+      Frag f0, f1;
+      int sa[MR], sa_last[MR];
+      auto read = [&](Frag& f, const unsigned char* st, int kk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int mt = 0; mt < MTV; ++mt) f.a[mt] = *reinterpret_cast<const i32x4_t*>(st + fa_off[kk] + mt * 128 * 128);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            f.b[nb][nt] = *reinterpret_cast<const i32x4_t*>(st + fb_off[kk] + (nb * BN + nt) * 128);
+          const unsigned char* sp = st + sb_off + (nb * 8 + kk) * BN;
+          f.sb[nb] = NT == 2 ? *reinterpret_cast<const uint16_t*>(sp) : *reinterpret_cast<const int*>(sp);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto mul = [&](const Frag& f, const int* s4, auto kk_) __attribute__((always_inline)) {
+        constexpr int kk = decltype(kk_)::value;
+        const i32x4_t z = {0, 0, 0, 0};
+        auto column = [&](auto nt_) __attribute__((always_inline)) {
+          constexpr int nt = decltype(nt_)::value;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const i32x8_t bf = __builtin_shufflevector(f.b[nb][nt], z, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+            for (int mt = 0; mt < MTV; ++mt) {  // weights first: lane l holds row l % 32 of the output
+              const i32x8_t af = __builtin_shufflevector(f.a[mt], z, 0, 1, 2, 3, 4, 5, 6, 7);
+              acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af, acc[nb][mt][nt], 4, 4, nt, f.sb[nb],
+                                                                               kk, s4[mt]);
+            }
+          }
+        };
+        column(std::integral_constant<int, 0>{});
+        column(std::integral_constant<int, 1>{});
+        if constexpr (NT == 4) {
+          column(std::integral_constant<int, 2>{});
+          column(std::integral_constant<int, 3>{});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
       for (int kt = 0; kt < nk; ++kt) {
-        // stage kt has landed for every wave, and every wave is done with the other buffer
+        // stage kt has landed for every wave, and every wave has read all it needs of the other buffer
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_barrier<0>();
         if ((kt & 3) == 0) {
           if (kt > 0) ab ^= 1;
@@ -200,42 +257,24 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
         if (kt + 1 < nk) issue(cur, kt + 1, buf ^ 1);
         if constexpr (MTV > 0) {
           const unsigned char* st = smem + buf * M4_STAGE;
-          int sa[MTV];
+          read(f0, st, 0);
+          if (kt > 0) mul(f1, sa_last, std::integral_constant<int, 3>{});
 #pragma unroll
           for (int mt = 0; mt < MTV; ++mt) {
             sa[mt] = *reinterpret_cast<const int*>(sf_a + ab * M4_SF_A + (mt * 128 + ar) * 32 + (kt & 3) * 8 + 4 * g2);
             if (half && kt == nk - 1 && g2) sa[mt] = 0;  // the absent blocks' bytes are another row's
+            sa_last[mt] = sa[mt];
           }
-          auto step = [&](auto kk_) __attribute__((always_inline)) {
-            constexpr int kk = decltype(kk_)::value;
-            const i32x4_t z = {0, 0, 0, 0};
-            i32x8_t af[MTV];
-#pragma unroll
-            for (int mt = 0; mt < MTV; ++mt)
-              af[mt] = __builtin_shufflevector(
-                  *reinterpret_cast<const i32x4_t*>(st + (mt * 128 + ar) * 128 + f_off[kk]), z, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const int c = wn * (BN / 2) + nt * 32 + l32;
-                const i32x8_t bf = __builtin_shufflevector(
-                    *reinterpret_cast<const i32x4_t*>(st + M4_A_BYTES + (nb * BN + c) * 128 + f_off[kk]), z, 0, 1, 2, 3,
-                    4, 5, 6, 7);
-                const int sb = st[M4_SF_B + (nb * 8 + 4 * g2 + kk) * BN + c];
-#pragma unroll
-                for (int mt = 0; mt < MTV; ++mt)  // weights first: lane l holds row l % 32 of the output
-                  acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af[mt], acc[nb][mt][nt], 4, 4, 0,
-                                                                                   sb, kk, sa[mt]);
-              }
-          };
-          step(std::integral_constant<int, 0>{});
-          step(std::integral_constant<int, 1>{});
-          step(std::integral_constant<int, 2>{});
-          step(std::integral_constant<int, 3>{});
+          read(f1, st, 1);
+          mul(f0, sa, std::integral_constant<int, 0>{});
+          read(f0, st, 2);
+          mul(f1, sa, std::integral_constant<int, 1>{});
+          read(f1, st, 3);
+          mul(f0, sa, std::integral_constant<int, 2>{});
         }
         buf ^= 1;
       }
+      if constexpr (MTV > 0) mul(f1, sa_last, std::integral_constant<int, 3>{});
     };
     if (cur.nmt == 2) k_loop(std::integral_constant<int, 2>{});
     else if (cur.nmt == 1) k_loop(std::integral_constant<int, 1>{});
@@ -251,43 +290,51 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       issue(cur, 0, buf);
     }
 
-    // Lane l holds row l % 32 of its block; acc[..][4j + c] is column 8j + 4G + c of 32.
+    // Lane l holds row l % 32 of its block; acc[..][nt][4j + c] is column NT (8j + 4G + c) + nt of the wave's: for
+    // each j a run of 4 NT neighbouring columns.
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const int r = mt * 128 + ar;
       const bool ok = r < rows_valid;
       const size_t row = (size_t)row0 + (ok ? r : 0);
+      const int c0 = n0 + wn * (BN / 2);
+      if constexpr (GATED) {
+        // a block of 32 columns is the runs of j = 2p and 2p + 1 of this lane and of lane ^ 32
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int c0 = n0 + wn * (BN / 2) + nt * 32;
-        if constexpr (GATED) {
-          // a block of 32 columns is the lane's 16 values and lane ^ 32's
+        for (int p = 0; p < 2; ++p) {
           float v[16];
           uint32_t m = 0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            v[i] = silu_f32(acc[0][mt][nt][i]) * acc[1][mt][nt][i];
+            const int at = 8 * p + i / 2;  // 4j + c, two columns each
+            v[i] = silu_f32(acc[0][mt][i & 1][at]) * acc[1][mt][i & 1][at];
             m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
           }
-          const auto sw32 = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-          const uint32_t byte = mx_scale_byte(max((uint32_t)sw32[0], (uint32_t)sw32[1]));
-          // two runs of four columns per word, columns 8j + 4G; then the halves trade so that group 0 has
-          // columns 0..15 and group 1 columns 16..31
-          const uint32_t w0 = mx_pack8(v, byte), w1 = mx_pack8(v + 8, byte);
-          const auto tr = __builtin_amdgcn_permlane32_swap(w0, w1, false, false);
-          // tr[0]: columns 4.. of group 0's runs, tr[1]: of group 1's, interleaved by 16 bits
-          const uint32_t lo = __builtin_amdgcn_perm(tr[1], tr[0], 0x05040100);
-          const uint32_t hi = __builtin_amdgcn_perm(tr[1], tr[0], 0x07060302);
+          const auto both = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+          const uint32_t byte = mx_scale_byte(max((uint32_t)both[0], (uint32_t)both[1]));
+          // the halves trade runs: group 0 gets columns 0..15 of the block, group 1 columns 16..31
+          const auto tr = __builtin_amdgcn_permlane32_swap(mx_pack8(v, byte), mx_pack8(v + 8, byte), false, false);
           if (ok) {
-            *reinterpret_cast<uint2*>(a.h_q + row * (N / 2) + c0 / 2 + 8 * g2) = make_uint2(lo, hi);
-            if (g2 == 0) a.h_sf[row * (N / 32) + c0 / 32] = (uint8_t)byte;
+            const int c = c0 + 32 * p;
+            *reinterpret_cast<uint2*>(a.h_q + row * (N / 2) + c / 2 + 8 * g2) = make_uint2(tr[0], tr[1]);
+            if (g2 == 0) a.h_sf[row * (N / 32) + c / 32] = (uint8_t)byte;
           }
-        } else {
+        }
+      } else {
+        if (ok && c0 < N) {
+          uint16_t* yp = a.y + row * N + c0 + 16 * g2;
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint4 v = pack_row16(acc[0][mt][nt], 8 * p);
-            if (ok && c0 < N) *reinterpret_cast<uint4*>(a.y + row * N + c0 + 16 * p + 8 * g2) = v;
-          }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = 4 * j + 2 * h;
+              uint4 v;
+              v.x = pack_bf16x2(acc[0][mt][0][i], acc[0][mt][1][i]);
+              v.y = pack_bf16x2(acc[0][mt][2][i], acc[0][mt][3][i]);
+              v.z = pack_bf16x2(acc[0][mt][0][i + 1], acc[0][mt][1][i + 1]);
+              v.w = pack_bf16x2(acc[0][mt][2][i + 1], acc[0][mt][3][i + 1]);
+              *reinterpret_cast<uint4*>(yp + 32 * j + 8 * h) = v;
+            }
         }
       }
     }
