@@ -21,6 +21,7 @@
 #include "tile_sched.h"
 
 #include <type_traits>
+#include <utility>
 
 namespace moe {
 
@@ -43,6 +44,16 @@ constexpr int M4_SF_A = M4_BM * 32;               // activation scales of four s
 constexpr int M4_SCHED = M4_NS * (M4_STAGE + M4_SF_A);
 constexpr int M4_LDS = M4_SCHED + (M4_MAX_E + 1 + 16) * 4;
 static_assert(M4_LDS <= 160 * 1024, "LDS budget");
+
+// f(0), f(1), .. f(N - 1) with compile-time numbers.
+template <int N, typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl<N>(f, std::make_integer_sequence<int, N>{});
+}
 
 struct Mx4Args {
   const uint8_t *A, *A_sf;
@@ -208,43 +219,43 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
         int sb[NB];
       };
       Frag f0, f1;
-      int sa[MR], sa_last[MR];
-      auto read = [&](Frag& f, const unsigned char* st, int kk) __attribute__((always_inline)) {
-#pragma unroll
-        for (int mt = 0; mt < MTV; ++mt) f.a[mt] = *reinterpret_cast<const i32x4_t*>(st + fa_off[kk] + mt * 128 * 128);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            f.b[nb][nt] = *reinterpret_cast<const i32x4_t*>(st + fb_off[kk] + (nb * BN + nt) * 128);
-          const unsigned char* sp = st + sb_off + (nb * 8 + kk) * BN;
-          f.sb[nb] = NT == 2 ? *reinterpret_cast<const uint16_t*>(sp) : *reinterpret_cast<const int*>(sp);
+      int sa[MR];
+      // Read `i` of a step's fragments, in the order in which the products take them.
+      constexpr int READS = MTV + NB * (1 + NT);
+      auto read_one = [&](Frag& f, const unsigned char* st, int kk, auto i_) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_)::value;
+        if constexpr (i < MTV) {
+          f.a[i] = *reinterpret_cast<const i32x4_t*>(st + fa_off[kk] + i * 128 * 128);
+        } else if constexpr (i < MTV + NB) {
+          const unsigned char* sp = st + sb_off + ((i - MTV) * 8 + kk) * BN;
+          f.sb[i - MTV] = NT == 2 ? *reinterpret_cast<const uint16_t*>(sp) : *reinterpret_cast<const int*>(sp);
+        } else if constexpr (i < READS) {
+          constexpr int nt = (i - MTV - NB) / NB, nb = (i - MTV - NB) % NB;
+          f.b[nb][nt] = *reinterpret_cast<const i32x4_t*>(st + fb_off[kk] + (nb * BN + nt) * 128);
         }
-        __builtin_amdgcn_sched_barrier(0);
       };
-      auto mul = [&](const Frag& f, const int* s4, auto kk_) __attribute__((always_inline)) {
-        constexpr int kk = decltype(kk_)::value;
-        const i32x4_t z = {0, 0, 0, 0};
-        auto column = [&](auto nt_) __attribute__((always_inline)) {
-          constexpr int nt = decltype(nt_)::value;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const i32x8_t bf = __builtin_shufflevector(f.b[nb][nt], z, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-            for (int mt = 0; mt < MTV; ++mt) {  // weights first: lane l holds row l % 32 of the output
-              const i32x8_t af = __builtin_shufflevector(f.a[mt], z, 0, 1, 2, 3, 4, 5, 6, 7);
-              acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af, acc[nb][mt][nt], 4, 4, nt, f.sb[nb],
-                                                                               kk, s4[mt]);
-            }
+      // The products of one step, with the reads of the next spread between them: a wave that issued its reads
+      // in a row would wait for the LDS with its matrix core idle.
+      auto step = [&](const Frag& f, const int* s4, auto kk_, Frag& next, const unsigned char* st, auto next_)
+                      __attribute__((always_inline)) {
+        constexpr int kk = decltype(kk_)::value, kk_next = decltype(next_)::value;  // kk_next < 0: none
+        static_for<NB * NT * MTV>([&](auto m_) __attribute__((always_inline)) {
+          constexpr int m = decltype(m_)::value;
+          constexpr int mt = m % MR, nb = m / MR % NB, nt = m / MR / NB;
+          const i32x4_t z = {0, 0, 0, 0};
+          const i32x8_t bf = __builtin_shufflevector(f.b[nb][nt], z, 0, 1, 2, 3, 4, 5, 6, 7);
+          const i32x8_t af = __builtin_shufflevector(f.a[mt], z, 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(  // weights first: lane l holds row l % 32
+              bf, af, acc[nb][mt][nt], 4, 4, nt, f.sb[nb], kk, s4[mt]);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (kk_next >= 0) {
+            constexpr int per = MTV == 1 ? 2 : 1;
+            static_for<per>([&](auto i_) __attribute__((always_inline)) {
+              read_one(next, st, kk_next, std::integral_constant<int, per * m + decltype(i_)::value>{});
+            });
+            __builtin_amdgcn_sched_barrier(0);
           }
-        };
-        column(std::integral_constant<int, 0>{});
-        column(std::integral_constant<int, 1>{});
-        if constexpr (NT == 4) {
-          column(std::integral_constant<int, 2>{});
-          column(std::integral_constant<int, 3>{});
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        });
       };
       for (int kt = 0; kt < nk; ++kt) {
         // stage kt has landed for every wave, and every wave has read all it needs of the other buffer
@@ -257,24 +268,23 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
         if (kt + 1 < nk) issue(cur, kt + 1, buf ^ 1);
         if constexpr (MTV > 0) {
           const unsigned char* st = smem + buf * M4_STAGE;
-          read(f0, st, 0);
-          if (kt > 0) mul(f1, sa_last, std::integral_constant<int, 3>{});
+          if (kt > 0) {
+            step(f1, sa, std::integral_constant<int, 3>{}, f0, st, std::integral_constant<int, 0>{});
+          } else {
+            static_for<READS>([&](auto i_) __attribute__((always_inline)) { read_one(f0, st, 0, i_); });
+          }
 #pragma unroll
           for (int mt = 0; mt < MTV; ++mt) {
             sa[mt] = *reinterpret_cast<const int*>(sf_a + ab * M4_SF_A + (mt * 128 + ar) * 32 + (kt & 3) * 8 + 4 * g2);
             if (half && kt == nk - 1 && g2) sa[mt] = 0;  // the absent blocks' bytes are another row's
-            sa_last[mt] = sa[mt];
           }
-          read(f1, st, 1);
-          mul(f0, sa, std::integral_constant<int, 0>{});
-          read(f0, st, 2);
-          mul(f1, sa, std::integral_constant<int, 1>{});
-          read(f1, st, 3);
-          mul(f0, sa, std::integral_constant<int, 2>{});
+          step(f0, sa, std::integral_constant<int, 0>{}, f1, st, std::integral_constant<int, 1>{});
+          step(f1, sa, std::integral_constant<int, 1>{}, f0, st, std::integral_constant<int, 2>{});
+          step(f0, sa, std::integral_constant<int, 2>{}, f1, st, std::integral_constant<int, 3>{});
         }
         buf ^= 1;
       }
-      if constexpr (MTV > 0) mul(f1, sa_last, std::integral_constant<int, 3>{});
+      if constexpr (MTV > 0) step(f1, sa, std::integral_constant<int, 3>{}, f0, nullptr, std::integral_constant<int, -1>{});
     };
     if (cur.nmt == 2) k_loop(std::integral_constant<int, 2>{});
     else if (cur.nmt == 1) k_loop(std::integral_constant<int, 1>{});
