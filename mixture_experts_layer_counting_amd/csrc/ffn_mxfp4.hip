@@ -37,7 +37,8 @@ constexpr int M4_OUT = (int)0x80000000u;  // an offset past every range: loads z
 
 constexpr int M4_A_BYTES = M4_BM * M4_BK / 2;
 constexpr int M4_B_BYTES = M4_BN * M4_BK / 2;
-constexpr int M4_LD = M4_A_BYTES / (1024 * 8);   // wave loads per stage, each operand
+constexpr int M4_LD = M4_A_BYTES / (1024 * 8);    // wave loads per stage, each operand
+constexpr int M4_VM = 2 * M4_LD + 1;              // loads of a wave per stage, with the column scales
 constexpr int M4_SF_B = M4_A_BYTES + M4_B_BYTES;  // weight scales [8][BN per matrix] per matrix
 constexpr int M4_STAGE = M4_SF_B + M4_BN * 8;
 constexpr int M4_SF_A = M4_BM * 32;               // activation scales of four stages [256][32]
@@ -71,6 +72,8 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   constexpr int NB = GATED ? 2 : 1;
   constexpr int BN = M4_BN / NB;   // columns per matrix
   constexpr int NT = BN / 64;      // 32-column blocks of a wave per matrix
+  constexpr int MT = 2;            // 32-row blocks of a wave
+  constexpr int STORES = GATED ? 2 : 8;  // 8- and 16-byte stores of a row block, at least
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   unsigned char* sf_a = smem + M4_NS * M4_STAGE;
   int* tstart = reinterpret_cast<int*>(smem + M4_SCHED);
@@ -89,20 +92,19 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   const int slot = xcd_slot(blockIdx.x, G);
   const uint32_t lds0 = lds_addr(smem);
 
-  // Loads of a stage: wave load j = wave + 8 i covers rows (columns) 8j..8j+7, lane -> row 8j + lane/8, slot
-  // lane % 8 of which holds chunk slot ^ (row/2 mod 8), for columns slot ^ (column/NT mod 8): eight neighbouring
-  // lanes of a fragment read, NT columns apart, then hit eight different slots. Chunks 4..7 are
-  // absent in a half stage.
-  int ld_row[M4_LD], ld_chunk[M4_LD], ld_bchunk[M4_LD];
+  // Loads of a stage: wave load j = wave + 8 i fills LDS rows 8j..8j+7 of 128 bytes, lane -> row 8j + lane/8, slot
+  // lane % 8 of which holds chunk slot ^ (row/2 mod 8), for weights slot ^ (column/NT mod 8): eight
+  // neighbouring lanes of a fragment read, NT columns apart, then hit eight different slots. Chunks 4..7
+  // are absent in a half stage.
+  int ld_row[M4_LD];
 #pragma unroll
-  for (int i = 0; i < M4_LD; ++i) {
-    ld_row[i] = (wave + 8 * i) * 8 + (lane >> 3);
-    ld_chunk[i] = (lane & 7) ^ ((ld_row[i] >> 1) & 7);
-    ld_bchunk[i] = (lane & 7) ^ ((ld_row[i] / NT) & 7);
-  }
+  for (int i = 0; i < M4_LD; ++i) ld_row[i] = (wave + 8 * i) * 8 + (lane >> 3);
+  const int ld_chunk = (lane & 7) ^ ((ld_row[0] >> 1) & 7);   // rows 64 apart share it
+  const int ld_bchunk = (lane & 7) ^ ((ld_row[0] / NT) & 7);
+  const int b_off = ld_row[0] * kb + ld_bchunk * 16;
   // Scales of the columns: LDS [NB][8][BN], bytes 256 wave .. of the block. Scales of the rows: half
   // lane % 2 of the 32 bytes of row 32 wave + lane / 2, for four stages at once. They lie row by row, a cache
-  // line per row however few bytes are taken, and it is the lines asked for that bound the loads.
+  // line per row however few bytes are taken, and the lines asked for cost as much as the bytes.
   const int sa_row = wave * 32 + (lane >> 1), sa_half = lane & 1;
   const int sb_byte = wave * 256 + lane * 4;
   const int sb_nb = sb_byte / (8 * BN), sb_kb = (sb_byte / BN) & 7, sb_col = sb_byte % BN;
@@ -134,14 +136,14 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       const int ssrc = a.row_src[d.row0 + min(sa_row, d.rows_valid - 1)];
 #pragma unroll
       for (int i = 0; i < M4_LD; ++i)
-        d.a_off[i] = (ld_row[i] < d.rows_valid && src[i] >= 0) ? (src[i] / a.a_k) * kb + ld_chunk[i] * 16 : M4_OUT;
+        d.a_off[i] = (ld_row[i] < d.rows_valid && src[i] >= 0) ? (src[i] / a.a_k) * kb + ld_chunk * 16 : M4_OUT;
       d.s_off = (sa_row < d.rows_valid && ssrc >= 0) ? (ssrc / a.a_k) * ksf + sa_half * 16 : M4_OUT;
     } else {
       d.rA = make_rsrc(a.A + (size_t)d.row0 * kb, (uint32_t)d.rows_valid * (uint32_t)kb);
       d.rS = make_rsrc(a.A_sf + (size_t)d.row0 * ksf, (uint32_t)d.rows_valid * (uint32_t)ksf);
 #pragma unroll
       for (int i = 0; i < M4_LD; ++i)
-        d.a_off[i] = ld_row[i] < d.rows_valid ? ld_row[i] * kb + ld_chunk[i] * 16 : M4_OUT;
+        d.a_off[i] = ld_row[i] < d.rows_valid ? ld_row[i] * kb + ld_chunk * 16 : M4_OUT;
       d.s_off = sa_row < d.rows_valid ? sa_row * ksf + sa_half * 16 : M4_OUT;
     }
     d.nmt = __builtin_amdgcn_readfirstlane((wm * 32 < d.rows_valid) + (128 + wm * 32 < d.rows_valid));
@@ -151,25 +153,29 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     d.rB1 = GATED ? make_rsrc(a.B1 + wbase, range) : d.rB0;
     return d;
   };
-  auto issue = [&](const Tile& d, int kt, int buf) __attribute__((always_inline)) {
+  // Piece j of this wave's loads of stage kt into buffer buf: row loads, column loads, column scales.
+  auto piece = [&](const Tile& d, int kt, int buf, auto j_) __attribute__((always_inline)) {
+    constexpr int j = decltype(j_)::value;
     const uint32_t so = lds0 + (uint32_t)buf * M4_STAGE;
     const bool cut = half && kt == nk - 1;
-#pragma unroll
-    for (int i = 0; i < M4_LD; ++i)
-      lds_dma16(d.rA, so + (wave + 8 * i) * 1024, cut && ld_chunk[i] >= 4 ? M4_OUT : d.a_off[i], kt * (M4_BK / 2));
-#pragma unroll
-    for (int i = 0; i < M4_LD; ++i) {
-      const bool second = GATED && i >= M4_LD / 2;
-      const int c = ld_row[i] - (second ? BN : 0);
+    if constexpr (j < M4_LD) {
+      lds_dma16(d.rA, so + (wave + 8 * j) * 1024, cut && ld_chunk >= 4 ? M4_OUT : d.a_off[j], kt * (M4_BK / 2));
+    } else if constexpr (j < 2 * M4_LD) {
+      constexpr int i = j - M4_LD;
+      constexpr bool second = GATED && i >= M4_LD / 2;
+      constexpr int c0 = i * 64 - (second ? BN : 0);  // columns c0 + ld_row[0], 64 of them inside the matrix or none
       lds_dma16(second ? d.rB1 : d.rB0, so + M4_A_BYTES + (wave + 8 * i) * 1024,
-                cut && ld_bchunk[i] >= 4 ? M4_OUT : c * kb + ld_bchunk[i] * 16, kt * (M4_BK / 2));
+                (cut && ld_bchunk >= 4) || (!GATED && d.n0 + c0 >= N) ? M4_OUT : b_off, kt * (M4_BK / 2) + c0 * kb);
+    } else {
+      const int planes = min(8, ksf - 8 * kt);
+      const uint8_t* sfb = (GATED && sb_nb) ? a.B1_sf : a.B0_sf;
+      lds_dma4(make_rsrc(sfb + ((size_t)d.e * ksf + 8 * (size_t)kt) * N, (uint32_t)N * (uint32_t)planes),
+               so + M4_SF_B + wave * 256, sb_kb < planes && d.n0 + sb_col < N ? sb_kb * N + d.n0 + sb_col : M4_OUT, 0);
     }
-    const int planes = min(8, ksf - 8 * kt);
-    const uint8_t* sfb = (GATED && sb_nb) ? a.B1_sf : a.B0_sf;
-    lds_dma4(make_rsrc(sfb + ((size_t)d.e * ksf + 8 * (size_t)kt) * N, (uint32_t)N * (uint32_t)planes),
-             so + M4_SF_B + wave * 256, sb_kb < planes && d.n0 + sb_col < N ? sb_kb * N + d.n0 + sb_col : M4_OUT, 0);
   };
-
+  auto issue = [&](const Tile& d, int kt, int buf) __attribute__((always_inline)) {
+    static_for<M4_VM>([&](auto j_) __attribute__((always_inline)) { piece(d, kt, buf, j_); });
+  };
   // The row scales of stages 4q..4q+3, into half `ab`; bytes past the last row's read as zero, so the whole
   // offset is in the checked part.
   auto issue_sf = [&](const Tile& d, int q, int ab) __attribute__((always_inline)) {
@@ -190,7 +196,7 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   }
   const int sb_off = M4_SF_B + 4 * g2 * BN + wcol;
 
-  int buf = 0, ab = 0;
+  int buf = 0, ab = 0, stored = 0;  // stored: row blocks that this wave stored after the prologue's loads
   Tile cur;
   if (slot < total) {
     cur = decode(slot);
@@ -198,11 +204,11 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     issue(cur, 0, buf);
   }
   for (int t = slot; t < total; t += G) {
-    f32x16_t acc[NB][2][NT];
+    f32x16_t acc[NB][MT][NT];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -234,12 +240,14 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
           f.b[nb][nt] = *reinterpret_cast<const i32x4_t*>(st + fb_off[kk] + (nb * BN + nt) * 128);
         }
       };
-      // The products of one step, with the reads of the next spread between them: a wave that issued its reads
-      // in a row would wait for the LDS with its matrix core idle.
-      auto step = [&](const Frag& f, const int* s4, auto kk_, Frag& next, const unsigned char* st, auto next_)
-                      __attribute__((always_inline)) {
+      // The products of one step, with the reads of the next spread between them, and with the loads of stage
+      // kt + 1 (LOAD): a wave that issued them in a row would hold up its matrix core.
+      auto step = [&](const Frag& f, const int* s4, auto kk_, Frag& next, const unsigned char* st, auto next_,
+                      auto load_, int kt) __attribute__((always_inline)) {
         constexpr int kk = decltype(kk_)::value, kk_next = decltype(next_)::value;  // kk_next < 0: none
-        static_for<NB * NT * MTV>([&](auto m_) __attribute__((always_inline)) {
+        constexpr bool LOAD = decltype(load_)::value;
+        constexpr int PRODUCTS = NB * NT * MR;
+        static_for<PRODUCTS>([&](auto m_) __attribute__((always_inline)) {
           constexpr int m = decltype(m_)::value;
           constexpr int mt = m % MR, nb = m / MR % NB, nt = m / MR / NB;
           const i32x4_t z = {0, 0, 0, 0};
@@ -249,89 +257,121 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
               bf, af, acc[nb][mt][nt], 4, 4, nt, f.sb[nb], kk, s4[mt]);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (kk_next >= 0) {
-            constexpr int per = MTV == 1 ? 2 : 1;
+            constexpr int per = (READS + PRODUCTS - 1) / PRODUCTS;
             static_for<per>([&](auto i_) __attribute__((always_inline)) {
               read_one(next, st, kk_next, std::integral_constant<int, per * m + decltype(i_)::value>{});
             });
-            __builtin_amdgcn_sched_barrier(0);
           }
+          if constexpr (LOAD) {
+            constexpr int per = (M4_VM + PRODUCTS - 1) / PRODUCTS;
+            static_for<per>([&](auto i_) __attribute__((always_inline)) {
+              constexpr int j = per * m + decltype(i_)::value;
+              if constexpr (j < M4_VM) piece(cur, kt + 1, buf ^ 1, std::integral_constant<int, j>{});
+            });
+          }
+          __builtin_amdgcn_sched_barrier(0);
         });
       };
-      for (int kt = 0; kt < nk; ++kt) {
-        // stage kt has landed for every wave, and every wave has read all it needs of the other buffer
+      using std::integral_constant;
+      auto scales = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int mt = 0; mt < MTV; ++mt) {
+          sa[mt] = *reinterpret_cast<const int*>(sf_a + ab * M4_SF_A + (mt * 128 + ar) * 32 + (kt & 3) * 8 + 4 * g2);
+          if (half && kt == nk - 1 && g2) sa[mt] = 0;  // the absent blocks' bytes are another row's
+        }
+      };
+      auto rest = [&](const unsigned char* st, int kt) __attribute__((always_inline)) {
+        step(f0, sa, integral_constant<int, 0>{}, f1, st, integral_constant<int, 1>{}, std::false_type{}, kt);
+        step(f1, sa, integral_constant<int, 1>{}, f0, st, integral_constant<int, 2>{}, std::false_type{}, kt);
+        step(f0, sa, integral_constant<int, 2>{}, f1, st, integral_constant<int, 3>{}, std::false_type{}, kt);
+      };
+      // Stage kt has landed for every wave, and every wave has read all it needs of the other buffer.
+      auto stage = [&](int kt, auto load_) __attribute__((always_inline)) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_barrier<0>();
         if ((kt & 3) == 0) {
-          if (kt > 0) ab ^= 1;
+          ab ^= 1;
           if (kt + 4 < nk) issue_sf(cur, kt / 4 + 1, ab ^ 1);
         }
-        if (kt + 1 < nk) issue(cur, kt + 1, buf ^ 1);
         if constexpr (MTV > 0) {
           const unsigned char* st = smem + buf * M4_STAGE;
-          if (kt > 0) {
-            step(f1, sa, std::integral_constant<int, 3>{}, f0, st, std::integral_constant<int, 0>{});
-          } else {
-            static_for<READS>([&](auto i_) __attribute__((always_inline)) { read_one(f0, st, 0, i_); });
-          }
-#pragma unroll
-          for (int mt = 0; mt < MTV; ++mt) {
-            sa[mt] = *reinterpret_cast<const int*>(sf_a + ab * M4_SF_A + (mt * 128 + ar) * 32 + (kt & 3) * 8 + 4 * g2);
-            if (half && kt == nk - 1 && g2) sa[mt] = 0;  // the absent blocks' bytes are another row's
-          }
-          step(f0, sa, std::integral_constant<int, 0>{}, f1, st, std::integral_constant<int, 1>{});
-          step(f1, sa, std::integral_constant<int, 1>{}, f0, st, std::integral_constant<int, 2>{});
-          step(f0, sa, std::integral_constant<int, 2>{}, f1, st, std::integral_constant<int, 3>{});
+          step(f1, sa, integral_constant<int, 3>{}, f0, st, integral_constant<int, 0>{}, load_, kt);
+          scales(kt);
+          rest(st, kt);
+        } else if constexpr (decltype(load_)::value) {
+          issue(cur, kt + 1, buf ^ 1);
         }
         buf ^= 1;
+      };
+      // The first stage: the previous tile's stores, younger than its loads, need not be done (memory operations
+      // complete in order). Then the stages that load another one, then the last.
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (stored == 0) wait_barrier<0>();
+      else if (stored == 1) wait_barrier<STORES>();
+      else wait_barrier<2 * STORES>();
+      if (nk > 4) issue_sf(cur, 1, ab ^ 1);
+      if (nk > 1) issue(cur, 1, buf ^ 1);
+      if constexpr (MTV > 0) {
+        const unsigned char* st = smem + buf * M4_STAGE;
+        static_for<READS>([&](auto i_) __attribute__((always_inline)) { read_one(f0, st, 0, i_); });
+        scales(0);
+        rest(st, 0);
       }
-      if constexpr (MTV > 0) step(f1, sa, std::integral_constant<int, 3>{}, f0, nullptr, std::integral_constant<int, -1>{});
+      buf ^= 1;
+      for (int kt = 1; kt + 1 < nk; ++kt) stage(kt, std::true_type{});
+      if (nk > 1) stage(nk - 1, std::false_type{});
+      if constexpr (MTV > 0)
+        step(f1, sa, integral_constant<int, 3>{}, f0, smem, integral_constant<int, -1>{}, std::false_type{}, 0);
     };
     if (cur.nmt == 2) k_loop(std::integral_constant<int, 2>{});
     else if (cur.nmt == 1) k_loop(std::integral_constant<int, 1>{});
     else k_loop(std::integral_constant<int, 0>{});
 
-    const int row0 = cur.row0, rows_valid = cur.rows_valid, n0 = cur.n0;
-    // The next tile's first stage goes into the buffer that stage nk-1 did not use, whose readers all
-    // passed the last barrier.
+    const int row0 = cur.row0, rows_valid = cur.rows_valid, n0 = cur.n0, nmt = cur.nmt;
+    // The next tile's first stage goes into the buffer that stage nk - 1 did not use, whose readers all
+    // passed the last barrier. So do those of the row scales' other half.
     if (t + G < total) {
       cur = decode(t + G);
       ab ^= 1;
       issue_sf(cur, 0, ab);
       issue(cur, 0, buf);
     }
+    const bool wave_in = GATED || n0 + wn * (BN / 2) < N;  // the wave's columns are inside the matrix
+    stored = wave_in ? nmt : 0;
 
     // Lane l holds row l % 32 of its block; acc[..][nt][4j + c] is column NT (8j + 4G + c) + nt of the wave's: for
     // each j a run of 4 NT neighbouring columns.
+    if (wave_in) {
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const int r = mt * 128 + ar;
-      const bool ok = r < rows_valid;
-      const size_t row = (size_t)row0 + (ok ? r : 0);
-      const int c0 = n0 + wn * (BN / 2);
-      if constexpr (GATED) {
-        // a block of 32 columns is the runs of j = 2p and 2p + 1 of this lane and of lane ^ 32
+      for (int mt = 0; mt < MT; ++mt) {
+        if (mt >= nmt) break;
+        const int r = mt * 128 + ar;
+        const bool ok = r < rows_valid;
+        const size_t row = (size_t)row0 + (ok ? r : 0);
+        const int c0 = n0 + wn * (BN / 2);
+        if constexpr (GATED) {
+          // a block of 32 columns is the runs of j = 2p and 2p + 1 of this lane and of lane ^ 32
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          float v[16];
-          uint32_t m = 0;
+          for (int p = 0; p < 2; ++p) {
+            float v[16];
+            uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = 8 * p + i / 2;  // 4j + c, two columns each
-            v[i] = silu_f32(acc[0][mt][i & 1][at]) * acc[1][mt][i & 1][at];
-            m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+            for (int i = 0; i < 16; ++i) {
+              const int at = 8 * p + i / 2;  // 4j + c, two columns each
+              v[i] = silu_f32(acc[0][mt][i & 1][at]) * acc[1][mt][i & 1][at];
+              m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+            }
+            const auto both = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+            const uint32_t byte = mx_scale_byte(max((uint32_t)both[0], (uint32_t)both[1]));
+            // the halves trade runs: group 0 gets columns 0..15 of the block, group 1 columns 16..31
+            const auto tr = __builtin_amdgcn_permlane32_swap(mx_pack8(v, byte), mx_pack8(v + 8, byte), false, false);
+            if (ok) {
+              const int c = c0 + 32 * p;
+              *reinterpret_cast<uint2*>(a.h_q + row * (N / 2) + c / 2 + 8 * g2) = make_uint2(tr[0], tr[1]);
+              if (g2 == 0) a.h_sf[row * (N / 32) + c / 32] = (uint8_t)byte;
+            }
           }
-          const auto both = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-          const uint32_t byte = mx_scale_byte(max((uint32_t)both[0], (uint32_t)both[1]));
-          // the halves trade runs: group 0 gets columns 0..15 of the block, group 1 columns 16..31
-          const auto tr = __builtin_amdgcn_permlane32_swap(mx_pack8(v, byte), mx_pack8(v + 8, byte), false, false);
-          if (ok) {
-            const int c = c0 + 32 * p;
-            *reinterpret_cast<uint2*>(a.h_q + row * (N / 2) + c / 2 + 8 * g2) = make_uint2(tr[0], tr[1]);
-            if (g2 == 0) a.h_sf[row * (N / 32) + c / 32] = (uint8_t)byte;
-          }
-        }
-      } else {
-        if (ok && c0 < N) {
+        } else if (ok) {
           uint16_t* yp = a.y + row * N + c0 + 16 * g2;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
