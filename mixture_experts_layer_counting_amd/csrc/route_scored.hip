@@ -38,21 +38,25 @@ struct ScoredArgs {
   float scale;
 };
 
-// The largest x over the 64 lanes, uniform: DPP row shifts gather each row's maximum in its last
-// lane, the broadcasts of lanes 15 and 31 carry it over the rows to lane 63.
-__device__ __forceinline__ float wave_max(float x) {
-  auto step = [&](auto ctrl) {
-    constexpr int C = decltype(ctrl)::value;
-    x = fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(x), __float_as_int(x), C, 0xF, 0xF, false)));
-  };
-  step(std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8
-  step(std::integral_constant<int, 0x112>{});
-  step(std::integral_constant<int, 0x114>{});
-  step(std::integral_constant<int, 0x118>{});
-  step(std::integral_constant<int, 0x142>{});  // row_bcast 15, 31
-  step(std::integral_constant<int, 0x143>{});
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+// A float as a signed integer of the same order (-0 just below +0; no NaN), and back. Integer
+// maxima need no quieting of their operands and take the lane moves as operand modifiers.
+__device__ __forceinline__ int order_key(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
 }
+__device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// The largest x over the 64 lanes, uniform: within the rows of 16 by lane moves, over the rows in
+// scalar registers.
+__device__ __forceinline__ int wave_max_key(int x) {
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, DPP_XOR1, 0xF, 0xF, true));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, DPP_XOR2, 0xF, 0xF, true));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, DPP_HALF_MIRROR, 0xF, 0xF, true));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, DPP_MIRROR, 0xF, 0xF, true));
+  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
+__device__ __forceinline__ float wave_max(float x) { return key_value(wave_max_key(order_key(x))); }
 
 // LDS written by some lanes of this wave is read by others after this.
 __device__ __forceinline__ void wave_sync() {
@@ -64,7 +68,7 @@ __device__ __forceinline__ void wave_sync() {
 // A logit, masked (NaN, -inf, the type's lowest value) as -inf, +inf as the largest fp32.
 __device__ __forceinline__ float unmask(float x, int bf16) {
   const float lowest = bf16 ? -3.38953139e38f : -3.40282347e38f;
-  return x > lowest ? fminf(x, 3.40282347e38f) : NEG_INF;
+  return x > lowest ? __builtin_amdgcn_fmed3f(x, -3.40282347e38f, 3.40282347e38f) : NEG_INF;
 }
 
 __device__ __forceinline__ float read_logit(const void* row, int e, int bf16) {
@@ -75,7 +79,8 @@ __device__ __forceinline__ const void* logit_row(const ScoredArgs& a, int t) {
   return static_cast<const char*>(a.logits) + (size_t)t * a.E * (a.bf16 ? 2 : 4);
 }
 
-// The fp32 choices of one lane's experts, -inf where masked. top, total: the softmax's largest
+// The fp32 choices of one lane's experts, -inf where masked (or NaN by a NaN bias: like -inf it is greater
+// than nothing). top, total: the softmax's largest
 // logit and sum. (The branches are uniform and outside the loops: each loop is straight code.)
 template <int ITEMS>
 __device__ __forceinline__ void choices(const ScoredArgs& a, bool scores, const float (&l)[ITEMS],
@@ -96,7 +101,7 @@ __device__ __forceinline__ void choices(const ScoredArgs& a, bool scores, const 
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     c[i] = with_bias ? s[i] + bias[i] : l[i];
-    if (!(l[i] > NEG_INF && bias[i] > NEG_INF)) c[i] = NEG_INF;
+    if (!(l[i] > NEG_INF)) c[i] = NEG_INF;
   }
 }
 
@@ -163,20 +168,16 @@ __device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, F tol,
   if (a.lp >= 5) merge(pair_lane<16>(m1), pair_lane<16>(m2));
   const F score = a.group_top == 2 && m2 > ninf ? m1 + m2 : m1;
   int rank = 0;
-  bool near = false;
+  F under = ninf;  // the largest score that comes after this one
   for (int j = 0; j < a.G; ++j) {
     const F o = lane_value(score, j << a.lp);
-    rank += (o > score || (o == score && j < g)) ? 1 : 0;
-    near |= j != g && o - score <= 2 * tol && score - o <= 2 * tol;
+    const bool before = j < g ? o >= score : o > score;
+    rank += before ? 1 : 0;
+    if (tol > 0) under = !before && j != g && o > under ? o : under;
   }
   const bool kept = g < a.G && rank < a.topk_groups;
-  if (tol > 0 && __ballot(near && g < a.G)) {  // only a pair across the border matters
-    for (int j = 0; j < a.G; ++j) {
-      const F o = lane_value(score, j << a.lp);
-      const bool o_kept = __builtin_amdgcn_readlane((int)kept, j << a.lp);
-      close |= kept != o_kept && g < a.G && o - score <= 2 * tol && score - o <= 2 * tol;
-    }
-  }
+  // only the border matters: the last kept group and the one after it
+  if (tol > 0) close = rank == a.topk_groups - 1 && g < a.G && score > ninf && score - under <= 2 * tol;
   return kept;
 }
 
@@ -246,8 +247,8 @@ __device__ __forceinline__ int choose_exact(ScoredArgs a, const float* row, floa
   return my_e;
 }
 
-// For the scores that are returned: expf is good to about an ulp at any x.
-__device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
+// For the scores that are returned: expf is good to about an ulp at any x, the hardware's reciprocal too.
+__device__ __forceinline__ float sigmoid_f32(float l) { return __builtin_amdgcn_rcpf(1.0f + expf(-l)); }
 
 // The pick's score as a share of the picks' sum (lanes without a pick: on = false). Where every
 // sigmoid is so small that their sum may underflow, sigma(l) = exp(l) to the last bit and the
@@ -257,7 +258,7 @@ __device__ __forceinline__ float pick_share(float l, bool on, bool sigmoid) {
   const bool ratio = sigmoid && top > -60.0f;
   const float s = on ? (ratio ? sigmoid_f32(l) : expf(l - top)) : 0.f;
   const float sum = wave_sum(s);
-  return on ? s / sum : 0.f;
+  return on ? s * __builtin_amdgcn_rcpf(sum) : 0.f;
 }
 
 // One wave per token:
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
                                                                      float* __restrict__ topk_w) {
   __shared__ float rows[RS_WAVES][RS_MAX_E];
   __shared__ float2 cand[RS_WAVES][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * RS_WAVES + wave;
   if (t >= a.T) return;
   const void* row = logit_row(a, t);
@@ -320,7 +321,8 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) z += __expf(l[i] - top);
-    total = wave_sum(z);
+    z = wave_sum(z);
+    total = z > 0.f ? z : 1.f;  // (nothing left to pick from)
   }
   const bool scores = a.bias || (a.G > 1 && a.group_top == 2);
   float s[ITEMS], c[ITEMS];
@@ -346,14 +348,25 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
     const bool use_s = a.group_top == 2 && !a.bias;
     float m1 = NEG_INF, m2 = NEG_INF;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) top_two(c[i] > NEG_INF ? (use_s ? s[i] : c[i]) : NEG_INF, m1, m2);
+    for (int i = 0; i < ITEMS; ++i) {
+      const float u = c[i] > NEG_INF ? (use_s ? s[i] : c[i]) : NEG_INF;
+      m2 = __builtin_amdgcn_fmed3f(u, m1, m2);  // the second of the three, m1 >= m2
+      m1 = u > m1 ? u : m1;
+    }
     bool kept = group_kept<float>(a, lane, tol, m1, m2, close);
     if (__ballot(close)) {
       const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
       double d1 = (double)NEG_INF, d2 = d1;
+      // a lane's two largest in fp64 are among those within the bound of its second in fp32
+      const float low = a.bias ? m2 - 2.0f * tol : m2;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-        if (c[i] > NEG_INF) top_two(exact_score(a, l[i], top, sum) + (double)bias[i], d1, d2);
+      for (int i = 0; i < ITEMS; ++i) {
+        const bool in = c[i] > NEG_INF && (use_s ? s[i] >= low - 2.0f * tol : c[i] >= low);
+        if (__ballot(in)) {
+          const double d = exact_score(a, l[i], top, sum) + (double)bias[i];
+          if (in) top_two(d, d1, d2);
+        }
+      }
       kept = group_kept<double>(a, lane, 0.0, d1, d2, close);
     }
 #pragma unroll
@@ -363,15 +376,16 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
   bool plain = !(tol < 1e30f);  // an infinite or huge bias
   const float gap = a.bias ? tol : 0.f;
 
-  float own = NEG_INF;
+  float best = NEG_INF;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) own = fmaxf(own, c[i]);
-  float bar = NEG_INF;
+  for (int i = 0; i < ITEMS; ++i) best = c[i] > best ? c[i] : best;
+  const int none = order_key(NEG_INF);
+  int own = order_key(best), key = none;
   for (int k = 0; k < a.K; ++k) {
-    bar = wave_max(own);
-    own = own == bar ? NEG_INF : own;
+    key = wave_max_key(own);
+    own = own == key ? none : own;
   }
-  bar -= gap;
+  const float bar = key_value(key) - gap;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
@@ -394,23 +408,32 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
       v = x.x;
       e = __float_as_int(x.y);
     }
-    auto ranks = [&](auto x) {
-      bool near = false;
-      rank = 0;
-      for (int j = 0; j < n; ++j) {
-        const auto o = lane_value(x, j);
-        const int oe = __builtin_amdgcn_readlane(e, j);
-        rank += (o > x || (o == x && oe < e)) ? 1 : 0;
-        if constexpr (sizeof(x) == 4) near |= oe != e && __builtin_fabsf(o - x) <= gap;
+    // the candidates before this one: larger choices, equal ones with a lower id
+    // (+0 makes -0 and 0 equal)
+    const uint64_t mine64 = (uint64_t)(uint32_t)(order_key(v + 0.0f) ^ 0x80000000) << 32 | (uint32_t)~e;
+    const int hi = (int)(mine64 >> 32), lo = (int)mine64;
+    rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o =
+          (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, j) << 32 | (uint32_t)__builtin_amdgcn_readlane(lo, j);
+      rank += o > mine64 ? 1 : 0;
+    }
+    if (a.bias) {
+      // the neighbours in rank, through LDS
+      if (lane < n) cand[wave][rank].x = v;
+      wave_sync();
+      const float after = lane + 1 < n ? cand[wave][lane + 1].x : NEG_INF;
+      if (__ballot(lane + 1 < n && cand[wave][lane].x - after <= gap)) {
+        const float lv = lane < n ? mine[e] : 0.f;
+        const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
+        const double x = lane < n ? exact_score(a, lv, top, sum) + (double)a.bias[e] : (double)NEG_INF;
+        rank = 0;
+        for (int j = 0; j < n; ++j) {
+          const double o = lane_value(x, j);
+          const int oe = __builtin_amdgcn_readlane(e, j);
+          rank += (o > x || (o == x && oe < e)) ? 1 : 0;
+        }
       }
-      return near;
-    };
-    const bool near = ranks(v);
-    if (a.bias && __ballot(near && lane < n)) {
-      const float lv = lane < n ? mine[e] : 0.f;
-      const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
-      const double x = lane < n ? exact_score(a, lv, top, sum) + (double)a.bias[e] : (double)NEG_INF;
-      (void)ranks(x);
     }
     const bool on = lane < n && rank < a.K;
     my_e = on ? e : -1;
@@ -445,7 +468,7 @@ __global__ __launch_bounds__(64 * RS_WAVES) void route_scored_bwd_kernel(ScoredA
                                                                          const float* __restrict__ d_topk_w,
                                                                          void* __restrict__ d_logits) {
   __shared__ __attribute__((aligned(16))) float rows[RS_WAVES][RS_MAX_E];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * RS_WAVES + wave;
   if (t >= a.T) return;
   const void* row = logit_row(a, t);
@@ -489,11 +512,17 @@ __global__ __launch_bounds__(64 * RS_WAVES) void route_scored_bwd_kernel(ScoredA
     }
     for (int i = lane; i < a.E; i += 64) g[i] = 0.f;
   }
-  // picks in their order: the same expert twice adds up
+  // an expert's picks add up in their order, in each lane that holds one of them
+  float sum = 0.f;
+  const int mine = on ? e : -1;
   for (int k = 0; k < a.K; ++k) {
-    wave_sync();
-    if (lane == k && on) g[e] += v;
+    const float o = lane_value(v, k);
+    sum += __builtin_amdgcn_readlane(mine, k) == e ? o : 0.f;
   }
+  wave_sync();
+  const float at = on ? g[e] : 0.f;
+  wave_sync();
+  if (on) g[e] = at + sum;
   wave_sync();
   if (a.bf16) {
     uint16_t* out = static_cast<uint16_t*>(d_logits) + (size_t)t * a.E;

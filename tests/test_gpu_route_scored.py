@@ -69,7 +69,8 @@ FORMS = [dict(score=s, renorm=r, scale=c) for s, (r, c) in itertools.product(
 @pytest.mark.parametrize("T,E,K,G,tg,top", [
     (1, 1, 1, 1, 1, 1), (1, 64, 6, 1, 1, 1), (5, 2, 2, 2, 1, 1), (33, 7, 3, 1, 1, 1), (64, 60, 4, 6, 3, 2),
     (129, 384, 8, 8, 4, 2), (70, 256, 8, 8, 4, 1), (17, 1024, 32, 64, 9, 2), (9, 1023, 5, 33, 7, 2), (31, 130, 16, 13, 13, 2),
-    (40, 96, 12, 3, 1, 2), (8, 961, 32, 31, 2, 1)])
+    (40, 96, 12, 3, 1, 2), (8, 961, 32, 31, 2, 1), (2, 384, 16, 1, 1, 1), (3, 385, 9, 1, 1, 1), (5, 383, 16, 1, 1, 1),
+    (67, 160, 8, 16, 5, 2), (66, 160, 8, 8, 1, 1), (18, 336, 16, 14, 9, 2), (21, 340, 7, 17, 4, 2), (4, 372, 3, 4, 2, 1)])
 def test_route_scored(T, E, K, G, tg, top, dtype, form):
     if form["score"] == "sigmoid" and tg * (E // G) < K or tg * (E // G) < K:
         K = tg * (E // G)
@@ -78,6 +79,40 @@ def test_route_scored(T, E, K, G, tg, top, dtype, form):
     bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
     for b in (None, bias):
         check(lg, dtype, K, b, groups=G, topk_groups=tg, group_top=top, **form)
+
+
+def test_many_equal_choices():
+    """Hundreds of equal choices, more than the candidates that are kept: the lowest ids win."""
+    for E, K, G, tg in ((384, 8, 1, 1), (384, 8, 8, 4), (512, 20, 1, 1), (1024, 32, 16, 3)):
+        lg = np.zeros((6, E), np.float32)
+        lg[1, ::3] = 1.0
+        lg[2, -70:] = 2.0
+        lg[3] = -np.inf
+        lg[3, 5::7] = 0.25
+        for score in ("sigmoid", "softmax"):
+            for b in (None, np.zeros(E, np.float32)):
+                check(lg, "bf16", K, b, score=score, groups=G, topk_groups=tg, group_top=2, renorm=True)
+
+
+def test_zeros_of_both_signs_are_equal():
+    lg = np.full((4, 70), -1.0, np.float32)
+    lg[:, [3, 9, 20, 66]] = [-0.0, 0.0, -0.0, 0.0]
+    check(lg, "f32", 3, score="sigmoid")
+    check(lg, "f32", 3, score="softmax", groups=7, topk_groups=2, group_top=1)
+    check(lg, "bf16", 3, np.zeros(70, np.float32), score="softmax", groups=7, topk_groups=2, group_top=2)
+
+
+def test_infinite_and_huge_biases():
+    rng = np.random.default_rng(4)
+    for E, K, G, tg in ((96, 6, 4, 2), (448, 6, 4, 2)):
+        lg = rng.standard_normal((9, E)).astype(np.float32)
+        for spots in ({3: np.inf, 40: np.inf, 50: -np.inf}, {7: 3e38, 8: 3e38, 9: -3e38}, {1: 1e6, 60: 1e6}):
+            b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+            for e, v in spots.items():
+                b[e] = v
+            for score in ("sigmoid", "softmax"):
+                check(lg, "f32", K, b, score=score, groups=G, topk_groups=tg, group_top=2, renorm=False)
+                check(lg, "f32", K, b, score=score, renorm=True)
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
