@@ -14,8 +14,22 @@
 // x 128 columns, K stages of 256 (128 bytes of codes per row and per column: whole cache lines in
 // the stored layout), two stages in LDS filled by direct global->LDS loads, one in flight while
 // the other is consumed. Persistent grid, XCD-contiguous tile order and row blocks as in the fp8
-// kernel. Both operands are staged [256][128 B] with 16-byte chunk ^ (row/2 mod 8). A last half stage (K % 256
-// == 128) loads zeros for its absent blocks, codes and scales both.
+// kernel. Both operands are staged [256][128 B], 16-byte chunks swizzled by row. A last half stage
+// (K % 256 == 128) loads zeros for its absent blocks, codes and scales both.
+// Within a wave the loads of the next stage and the fragment reads of the next step are spread between the
+// products of this one, across the stage barrier too.
+//
+// What bounds it. With random codes the matrix cores alone, operands in registers, reach 6.5 PFLOP/s
+// here (zeros: 9.7): the power limit. A tile's stage is 2048 cycles of products for a SIMD's two
+// waves against about 1700 of LDS reads and 512 of LDS writes; without the stage loads the gate/up
+// kernel runs at 5.2 PFLOP/s, with them at 3.9-4.0 (65536 rows, 52 experts, H 7168, Hp 2048: 968
+// us), down with its 0.94 GB of output at 2.9 (660 us). With 384 experts (170 rows each) the weights' HBM
+// stream bounds it: gate/up 1.54 ms, 3.9 TB/s; down 0.92 ms, 4.3 TB/s.
+// Tried and slower (gate/up, 52 experts): stages of 128 with four in LDS, 64-byte requests (1039 us);
+// four waves of 128 x 128, a third less LDS traffic but one wave a SIMD and all 512 registers
+// (1109); touching the next stage's weight lines to bring them into L2 (989, and 1644 for 384 experts);
+// the next tile's first two stages before the stores (973). No difference: wave priorities, CUs started half a tile
+// apart.
 #include "lds_dma.h"
 #include "mxfp4.h"
 #include "tile_sched.h"
@@ -565,6 +579,7 @@ template <bool GATED>
 moe_status_t launch_stream(const Mx4Args& a, int M, hipStream_t s) {
   const int slots = M < a.E ? M : a.E;  // at most so many experts have rows
   const int64_t grid = (int64_t)slots * (a.N / (GATED ? 32 : 128));
+  // (two groups of 16 rows a pass cost more than one where most experts have fewer than eight)
   if (M <= 8 * slots)
     ffn_mxfp4_stream_kernel<GATED, 1><<<(unsigned)grid, S4_THREADS, 0, s>>>(a);
   else
@@ -572,15 +587,23 @@ moe_status_t launch_stream(const Mx4Args& a, int M, hipStream_t s) {
   return launch_status();
 }
 
-// Whether the streaming kernel takes M rows over E experts and N columns in tiles of bn. It does
-// where the tiles could not fill the chip: up to `slots` experts have rows, each with N / bn
-// tiles. On 256 CUs, H 7168, Hp 2048, gate/up: one token of 8 experts (128 tiles) 28 us against
-// the tiles' 47, two tokens (256) 54 against 53, eight (672) 161 against 142; H 2048, Hp 1024: one
-// token of 6 experts 7.9 against 15.7, four (168) 15.1 against 17.7, sixteen (424) 39 against 36. More than
-// 16 rows per expert would stream the weights more than once.
-bool streams(int M, int E, int N, int bn) {
+// Whether the streaming kernel takes M rows over E experts and N columns. It does where the tiles
+// could not fill the chip: up to `slots` experts have rows, each with N / bn tiles. Measured on 256
+// CUs, us, streamed against tiles, rows per expert in brackets:
+//   gate/up  8 experts, H 7168, Hp 2048 (128 tiles): [4] 27 / 39  [16] 34 / 39  [32] 48 / 39
+//            16 experts, the same (256 tiles): [1] 54 / 53;  42 experts (672): [1.5] 161 / 142
+//            4 experts, H 2560, Hp 1280 (40 tiles): [16] 8.0 / 15.8  [32] 10.9 / 15.5  [48] 16.5 / 16.3
+//   down     8 experts, Hp 2048, H 7168 (224 tiles): [1] 14.9 / 16.4  [4] 15.8 / 14.6  [16] 20 / 15
+//            4 experts, Hp 1280, H 2560 (40 tiles): [16] 8.2 / 9.8  [32] 11.4 / 10.1
+// Gate/up streams up to 16 rows per expert while the tiles do not outnumber the CUs and up to 32 while they are
+// a quarter of them; down, whose reduction is short, up to 2 and 16.
+bool streams(bool gated, int M, int E, int N) {
   const int slots = M < E ? M : E;
-  return M <= 16 * slots && (int64_t)slots * ((N + bn - 1) / bn) <= device_cu_count();
+  const int bn = gated ? M4_BN / 2 : M4_BN;
+  const int64_t tiles = (int64_t)slots * ((N + bn - 1) / bn);
+  const int cus = device_cu_count();
+  const int64_t few = gated ? 16 : 2, more = gated ? 32 : 16;
+  return (M <= few * slots && tiles <= cus) || (M <= more * slots && 4 * tiles <= cus);
 }
 
 template <bool GATED>
@@ -600,7 +623,7 @@ moe_status_t launch_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, c
                                       uint8_t* h_sf, hipStream_t s) {
   if (M == 0) return MOE_OK;
   const Mx4Args a{x_q, x_sf, row_src, K, T, cu, E, H, Hp, wg, sg, wu, su, h_q, h_sf, nullptr};
-  if (streams(M, E, Hp, M4_BN / 2) && (!row_src || T > 0)) return launch_stream<true>(a, M, s);
+  if (streams(true, M, E, Hp) && (!row_src || T > 0)) return launch_stream<true>(a, M, s);
   return launch_tiles<true>(a, s);
 }
 
@@ -609,7 +632,7 @@ moe_status_t launch_ffn_down_mxfp4(const uint8_t* h_q, const uint8_t* h_sf, cons
   if (M == 0) return MOE_OK;
   const Mx4Args a{h_q, h_sf, nullptr, 1, 0, cu, E, Hp, H, wd, sd, nullptr, nullptr, nullptr, nullptr,
                   static_cast<uint16_t*>(y)};
-  if (streams(M, E, H, M4_BN)) return launch_stream<false>(a, M, s);
+  if (streams(false, M, E, H)) return launch_stream<false>(a, M, s);
   return launch_tiles<false>(a, s);
 }
 

