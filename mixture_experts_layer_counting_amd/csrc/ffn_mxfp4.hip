@@ -22,13 +22,13 @@
 // What bounds it. With random codes the matrix cores alone, operands in registers, reach 6.5 PFLOP/s
 // here (zeros: 9.7): the power limit. A tile's stage is 2048 cycles of products for a SIMD's two
 // waves against about 1700 of LDS reads and 512 of LDS writes; without the stage loads the gate/up
-// kernel runs at 5.2 PFLOP/s, with them at 3.9-4.0 (65536 rows, 52 experts, H 7168, Hp 2048: 968
-// us), down with its 0.94 GB of output at 2.9 (660 us). With 384 experts (170 rows each) the weights' HBM
-// stream bounds it: gate/up 1.54 ms, 3.9 TB/s; down 0.92 ms, 4.3 TB/s.
+// kernel runs at 5.2 PFLOP/s, with them at 4.0 (65536 rows, 52 experts, H 7168, Hp 2048: 950
+// us), down with its 0.94 GB of output at 3.1 (620 us). With 384 experts (170 rows each) the weights' HBM
+// stream bounds it: gate/up 1.54 ms, 3.9 TB/s; down 0.87 ms, 4.5 TB/s.
 // Tried and slower (gate/up, 52 experts): stages of 128 with four in LDS, 64-byte requests (1039 us);
 // four waves of 128 x 128, a third less LDS traffic but one wave a SIMD and all 512 registers
 // (1109); touching the next stage's weight lines to bring them into L2 (989, and 1644 for 384 experts);
-// the next tile's first two stages before the stores (973). No difference: wave priorities, CUs started half a tile
+// the next tile's first two stages before the stores (973, beside 968). No difference: wave priorities, CUs started half a tile
 // apart.
 #include "lds_dma.h"
 #include "mxfp4.h"
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   constexpr int BN = M4_BN / NB;   // columns per matrix
   constexpr int NT = BN / 64;      // 32-column blocks of a wave per matrix
   constexpr int MT = 2;            // 32-row blocks of a wave
-  constexpr int STORES = GATED ? 2 : 8;  // 8- and 16-byte stores of a row block, at least
+  constexpr int STORES = GATED ? 2 : 16;  // 8-byte stores of a row block (down: a whole one), at least
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   unsigned char* sf_a = smem + M4_NS * M4_STAGE;
   int* tstart = reinterpret_cast<int*>(smem + M4_SCHED);
@@ -267,8 +267,13 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
           const i32x4_t z = {0, 0, 0, 0};
           const i32x8_t bf = __builtin_shufflevector(f.b[nb][nt], z, 0, 1, 2, 3, 4, 5, 6, 7);
           const i32x8_t af = __builtin_shufflevector(f.a[mt], z, 0, 1, 2, 3, 4, 5, 6, 7);
-          acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(  // weights first: lane l holds row l % 32
-              bf, af, acc[nb][mt][nt], 4, 4, nt, f.sb[nb], kk, s4[mt]);
+          // gate/up: weights first, lane l then holds output row l % 32; down: rows first, a lane holds a column
+          if constexpr (GATED)
+            acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af, acc[nb][mt][nt], 4, 4, nt, f.sb[nb],
+                                                                             kk, s4[mt]);
+          else
+            acc[nb][mt][nt] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(af, bf, acc[nb][mt][nt], 4, 4, kk, s4[mt],
+                                                                             nt, f.sb[nb]);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (kk_next >= 0) {
             constexpr int per = (READS + PRODUCTS - 1) / PRODUCTS;
@@ -351,10 +356,15 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       issue(cur, 0, buf);
     }
     const bool wave_in = GATED || n0 + wn * (BN / 2) < N;  // the wave's columns are inside the matrix
-    stored = wave_in ? nmt : 0;
+    if constexpr (GATED)
+      stored = nmt;
+    else
+      stored = wave_in ? (wm * 32 + 32 <= rows_valid) + (wm * 32 + 160 <= rows_valid) : 0;
 
-    // Lane l holds row l % 32 of its block; acc[..][nt][4j + c] is column NT (8j + 4G + c) + nt of the wave's: for
-    // each j a run of 4 NT neighbouring columns.
+    // Gate/up: lane l holds row l % 32 of its block; acc[..][nt][4j + c] is column NT (8j + 4G + c) + nt of the
+    // wave's: for each j a run of 4 NT neighbouring columns. Down: lane l holds columns 4 (l % 32) + nt, and
+    // acc[..][4j + c] is row 8j + 4G + c: a store writes 256 neighbouring bytes of
+    // two rows (65536 rows, 52 experts: 620 us; with a row per lane, 16 bytes in each of 32 rows, 660 us).
     if (wave_in) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -385,20 +395,17 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
               if (g2 == 0) a.h_sf[row * (N / 32) + c / 32] = (uint8_t)byte;
             }
           }
-        } else if (ok) {
-          uint16_t* yp = a.y + row * N + c0 + 16 * g2;
+        } else {
+          const int r0 = mt * 128 + wm * 32 + 4 * g2;  // this lane's rows: r0 + 8j + c
+          uint16_t* yp = a.y + (size_t)(row0 + r0) * N + c0 + 4 * l32;
+          const bool whole = mt * 128 + wm * 32 + 32 <= rows_valid;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = 4 * j + 2 * h;
-              uint4 v;
-              v.x = pack_bf16x2(acc[0][mt][0][i], acc[0][mt][1][i]);
-              v.y = pack_bf16x2(acc[0][mt][2][i], acc[0][mt][3][i]);
-              v.z = pack_bf16x2(acc[0][mt][0][i + 1], acc[0][mt][1][i + 1]);
-              v.w = pack_bf16x2(acc[0][mt][2][i + 1], acc[0][mt][3][i + 1]);
-              *reinterpret_cast<uint4*>(yp + 32 * j + 8 * h) = v;
-            }
+          for (int i = 0; i < 16; ++i) {
+            const int dr = 8 * (i >> 2) + (i & 3);
+            if (whole || r0 + dr < rows_valid)
+              *reinterpret_cast<uint2*>(yp + (size_t)dr * N) =
+                  make_uint2(pack_bf16x2(acc[0][mt][0][i], acc[0][mt][1][i]), pack_bf16x2(acc[0][mt][2][i], acc[0][mt][3][i]));
+          }
         }
       }
     }
