@@ -263,8 +263,9 @@ __device__ __forceinline__ float pick_share(float l, bool on, bool sigmoid) {
 
 // One wave per token:
 //  1. the choices in fp32, group limits;
-//  2. a threshold: the K-th largest of the lanes' own maxima, at most the K-th largest choice,
-//     found by K rounds of a wave maximum of one value per lane;
+//  2. a threshold: the K-th largest of the lanes' two largest, at most the K-th largest choice,
+//     found by K rounds of a wave maximum of one value per lane (with one value a lane, a few kept
+//     groups leave hardly more lanes than picks, and the bar falls too low for 64 candidates);
 //  3. the few choices from the threshold up (less the error bound) go to LDS and come back one per lane: the
 //     candidates, usually K to 2 K of them;
 //  4. a candidate's rank is the number of candidates before it. Where two of them lie within the error bound,
@@ -376,14 +377,19 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
   bool plain = !(tol < 1e30f);  // an infinite or huge bias
   const float gap = a.bias ? tol : 0.f;
 
-  float best = NEG_INF;
+  float best = NEG_INF, second = NEG_INF;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) best = c[i] > best ? c[i] : best;
+  for (int i = 0; i < ITEMS; ++i) {
+    second = __builtin_amdgcn_fmed3f(c[i], best, second);
+    best = c[i] > best ? c[i] : best;
+  }
   const int none = order_key(NEG_INF);
-  int own = order_key(best), key = none;
+  int own = order_key(best), next = order_key(second), key = none;
   for (int k = 0; k < a.K; ++k) {
     key = wave_max_key(own);
-    own = own == key ? none : own;
+    const bool taken = own == key;
+    own = taken ? next : own;
+    next = taken ? none : next;
   }
   const float bar = key_value(key) - gap;
   int n = 0;
