@@ -146,7 +146,7 @@ typedef struct {
  *  - A group scored with two choices but holding one unmasked expert has that one's choice.
  *  logits [T, E] of logits_dtype (F32 or BF16); bias [E] fp32 or NULL; topk_idx [T, K] int32 and
  *  topk_w [T, K] fp32 out. One kernel launch, deterministic; scores and weights in fp32.
- * Limits: 1 <= K <= 32, E <= 1024, groups <= 64 (MOE_EUNSUPPORTED beyond); E % groups == 0,
+ * Limits: 1 <= K <= 32, E <= 1024, groups <= 64, T <= 2^26 - 4 (MOE_EUNSUPPORTED beyond); E % groups == 0,
  * 1 <= topk_groups <= groups, group_top <= E / groups and K <= topk_groups * E / groups, a
  * finite scale (MOE_EINVAL otherwise). */
 MOE_API moe_status_t moe_route_scored(const moe_route_desc_t* d, const void* logits,
@@ -285,7 +285,7 @@ MOE_API moe_status_t moe_quantize_fp8(const void* x, moe_dtype_t x_dtype, int32_
  * with an infinity or a NaN gets scale byte 255 (NaN) and zero codes.
  *  x [R, C] of x_dtype (BF16 or F32), 16-byte aligned, C % 32 == 0;
  *  q [R, C/2] out, 4-byte aligned: byte j of a row holds column 2j in its low nibble;
- *  sf [R, C/32] out: X = 2^(byte - 127). One kernel launch, HBM-bound. */
+ *  sf [R, C/32] out: X = 2^(byte - 127). R * C < 2^35 - 2048. One kernel launch, HBM-bound. */
 MOE_API moe_status_t moe_quantize_mxfp4(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t C,
                                         uint8_t* q, uint8_t* sf, hipStream_t stream);
 
@@ -299,7 +299,8 @@ MOE_API moe_status_t moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, i
  *  w [E, K, N] of w_dtype (BF16 or F32), K the reduction: the layout of the bf16 and fp32 experts;
  *  layout MOE_MXFP4: q [E, N, K/2] out, or MOE_MXFP4_PAIRED: q [E, N/2, K/128, 2, 64] out
  *  (K % 128 == 0 and N % 2 == 0), bitwise what moe_pack_mxfp4_pairs makes of the former;
- *  sf [E, K/32, N] out in both. w and q 16-byte aligned, K % 32 == 0, E <= 65535. */
+ *  sf [E, K/32, N] out in both. w and q 16-byte aligned, K % 32 == 0, K < 2^24 - 256,
+ *  N <= 2^30, E <= 65535. */
 MOE_API moe_status_t moe_quantize_mxfp4_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K,
                                                 int32_t N, moe_dtype_t layout, uint8_t* q, uint8_t* sf,
                                                 hipStream_t stream);
@@ -457,8 +458,8 @@ MOE_API moe_status_t moe_grouped_ffn_fused_scatter(const void* x, moe_dtype_t ac
  *  sf_down [E, Hp/32, H] in the MOE_MXFP4 layout (not the paired one);
  *  h_q [M, Hp/2], h_sf [M, Hp/32]; y_rows [M, H] bf16. Rows past cu_seqlens[E] are not written.
  *  Every pointer to codes 16-byte aligned, scales and y_rows too.
- * Needs H % 128 == 0 and Hp % 128 == 0, E <= 1024, and T*H/2 and H*Hp/2 (the codes of x and of an
- * expert matrix) below 2^31 (MOE_EUNSUPPORTED otherwise). One kernel launch each; with few rows per expert a kernel
+ * Needs H % 128 == 0 and Hp % 128 == 0, E <= 1024, and T*H/2 (gathered), H*Hp/2, 128*H and 128*Hp (the
+ * codes of x, of an expert matrix and of 256 rows) below 2^31, M < 2^30 (MOE_EUNSUPPORTED otherwise). One kernel launch each; with few rows per expert a kernel
  * that streams the weights past the rows, else tiles on the matrix cores, with the same result
  * up to the order of the fp32 sums. */
 MOE_API moe_status_t moe_ffn_gate_up_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, const int32_t* row_src,

@@ -197,6 +197,7 @@ static moe_status_t check_route_desc(const moe_route_desc_t* d, moe_dtype_t lt) 
   if (d->group_top < 1 || d->group_top > 2 || d->group_top > size) return MOE_EINVAL;
   if (d->K > (int64_t)d->topk_groups * size) return MOE_EINVAL;
   if (d->K > 32 || d->E > 1024 || d->groups > 64) return MOE_EUNSUPPORTED;
+  if (d->T > (1 << 26) - 4) return MOE_EUNSUPPORTED;  // 64 threads per token, counted in 32 bits
   if (lt != MOE_F32 && lt != MOE_BF16) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
@@ -349,7 +350,7 @@ static bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 static moe_status_t check_mxfp4_rows(moe_dtype_t dt, int64_t R, int64_t C) {
   if (R < 0 || C < 1) return MOE_EINVAL;
   if (C % 32 || (dt != MOE_BF16 && dt != MOE_F32)) return MOE_EUNSUPPORTED;
-  if (R * (C / 32) > (int64_t)std::numeric_limits<int32_t>::max() * 64) return MOE_EUNSUPPORTED;
+  if (R * (C / 32) > (1ll << 30) - 64) return MOE_EUNSUPPORTED;  // four threads per block, counted in 32 bits
   return MOE_OK;
 }
 
@@ -375,7 +376,7 @@ static moe_status_t check_mxfp4_weights(moe_dtype_t dt, moe_dtype_t layout, int 
   if (E < 0 || K < 0 || N < 0) return MOE_EINVAL;
   if (dt != MOE_BF16 && dt != MOE_F32) return MOE_EUNSUPPORTED;
   if (layout != MOE_MXFP4 && layout != MOE_MXFP4_PAIRED) return MOE_EUNSUPPORTED;
-  if (K % 32 || E > 65535 || K / 256 >= 65535) return MOE_EUNSUPPORTED;
+  if (K % 32 || E > 65535 || K / 256 >= 65535 || N > 1 << 30) return MOE_EUNSUPPORTED;
   if (layout == MOE_MXFP4_PAIRED && (K % 128 || N % 2)) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }

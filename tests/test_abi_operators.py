@@ -108,3 +108,17 @@ def test_ffn_mxfp4_refusals():
         moe.moe_grouped_ffn_mxfp4, P, P, P, 4, 2, P, M, 4, 256, 128, P, P, wd, P, P, P, y, ws, nb, 0)
     assert gr(nb=n - 1) == WS and gr(ws=None) == WS and gr(y=None) == INVAL and gr(wd=P + 8) == INVAL
     assert gr(ws=P + 8) == INVAL and gr(M=0, ws=None, nb=0) == OK
+
+
+def test_sizes_past_one_launch_are_refused():
+    """A launch's threads along an axis are counted in 32 bits: larger sizes are refused, not cut."""
+    d = route(T=2 ** 26)
+    assert status(moe.moe_route_scored, d, P, moe.MOE_F32, P, P, P, 0) == UNSUP
+    assert status(moe.moe_route_scored_backward, d, P, moe.MOE_F32, P, P, P, 0) == UNSUP
+    for f, args in ((moe.moe_quantize_mxfp4, lambda r, c: (P, moe.MOE_BF16, r, c, P, P, 0)),
+                    (moe.moe_dequantize_mxfp4, lambda r, c: (P, P, r, c, P, moe.MOE_BF16, 0))):
+        assert status(f, *args(2 ** 30, 32)) == UNSUP            # 2^35 values
+        assert status(f, *args(2 ** 20, 2 ** 15)) == UNSUP
+    for n in (2 ** 30 + 2, 2 ** 31 - 2):                         # column numbers past 32 bits in a lane
+        assert status(moe.moe_quantize_mxfp4_weights, P, moe.MOE_BF16, 1, 128, n, moe.MOE_MXFP4, P, P, 0) == UNSUP
+        assert status(moe.moe_dequantize_mxfp4_weights, P, P, moe.MOE_MXFP4_PAIRED, 1, 128, n, P, moe.MOE_F32, 0) == UNSUP
