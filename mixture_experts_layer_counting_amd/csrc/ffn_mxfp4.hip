@@ -107,15 +107,15 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
   const uint32_t lds0 = lds_addr(smem);
 
   // Loads of a stage: wave load j = wave + 8 i fills LDS rows 8j..8j+7 of 128 bytes, lane -> row 8j + lane/8, slot
-  // lane % 8 of which holds chunk slot ^ (row/2 mod 8), for weights slot ^ (column/NT mod 8): eight
-  // neighbouring lanes of a fragment read, NT columns apart, then hit eight different slots. Chunks 4..7
-  // are absent in a half stage.
+  // lane % 8 of which holds chunk slot ^ (row/2 mod 8): sixteen neighbouring lanes of a fragment read, a row
+  // each, then hit all 64 banks once. The columns lie in the order in which the fragments take them: LDS row
+  // 32 nt + l of a wave's holds its column NT l + nt (in column order the lanes of a read, NT columns apart,
+  // met in half of the banks). Chunks 4..7 are absent in a half stage.
   int ld_row[M4_LD];
 #pragma unroll
   for (int i = 0; i < M4_LD; ++i) ld_row[i] = (wave + 8 * i) * 8 + (lane >> 3);
   const int ld_chunk = (lane & 7) ^ ((ld_row[0] >> 1) & 7);   // rows 64 apart share it
-  const int ld_bchunk = (lane & 7) ^ ((ld_row[0] / NT) & 7);
-  const int b_off = ld_row[0] * kb + ld_bchunk * 16;
+  const int b_off = (NT * (ld_row[0] & 31) + (ld_row[0] >> 5)) * kb + ld_chunk * 16;
   // Scales of the columns: LDS [NB][8][BN], bytes 256 wave .. of the block. Scales of the rows: half
   // lane % 2 of the 32 bytes of row 32 wave + lane / 2, for four stages at once. They lie row by row, a cache
   // line per row however few bytes are taken, and the lines asked for cost as much as the bytes.
@@ -177,9 +177,11 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     } else if constexpr (j < 2 * M4_LD) {
       constexpr int i = j - M4_LD;
       constexpr bool second = GATED && i >= M4_LD / 2;
-      constexpr int c0 = i * 64 - (second ? BN : 0);  // columns c0 + ld_row[0], 64 of them inside the matrix or none
+      // rows 64 i..64 i + 63: 32-column blocks 2 i and 2 i + 1, NT of them a wave's
+      constexpr int blk = 2 * i - (second ? BN / 32 : 0);
+      constexpr int c0 = blk / NT * (BN / 2) + blk % NT;
       lds_dma16(second ? d.rB1 : d.rB0, so + M4_A_BYTES + (wave + 8 * i) * 1024,
-                (cut && ld_bchunk >= 4) || (!GATED && d.n0 + c0 >= N) ? M4_OUT : b_off, kt * (M4_BK / 2) + c0 * kb);
+                (cut && ld_chunk >= 4) || (!GATED && d.n0 + c0 >= N) ? M4_OUT : b_off, kt * (M4_BK / 2) + c0 * kb);
     } else {
       const int planes = min(8, ksf - 8 * kt);
       const uint8_t* sfb = (GATED && sb_nb) ? a.B1_sf : a.B0_sf;
@@ -206,7 +208,7 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     fa_off[kk] = ar * 128 + (((4 * g2 + kk) ^ ((l32 >> 1) & 7)) << 4);  // the same for every 32-row block
-    fb_off[kk] = M4_A_BYTES + wcol * 128 + (((4 * g2 + kk) ^ (l32 & 7)) << 4);
+    fb_off[kk] = M4_A_BYTES + (wn * (BN / 2) + l32) * 128 + (((4 * g2 + kk) ^ ((l32 >> 1) & 7)) << 4);
   }
   const int sb_off = M4_SF_B + 4 * g2 * BN + wcol;
 
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
           f.sb[i - MTV] = NT == 2 ? *reinterpret_cast<const uint16_t*>(sp) : *reinterpret_cast<const int*>(sp);
         } else if constexpr (i < READS) {
           constexpr int nt = (i - MTV - NB) / NB, nb = (i - MTV - NB) % NB;
-          f.b[nb][nt] = *reinterpret_cast<const i32x4_t*>(st + fb_off[kk] + (nb * BN + nt) * 128);
+          f.b[nb][nt] = *reinterpret_cast<const i32x4_t*>(st + fb_off[kk] + (nb * BN + nt * 32) * 128);
         }
       };
       // The products of one step, with the reads of the next spread between them, and with the loads of stage
