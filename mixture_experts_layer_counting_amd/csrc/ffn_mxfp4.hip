@@ -20,16 +20,18 @@
 // products of this one, across the stage barrier too.
 //
 // What bounds it. With random codes the matrix cores alone, operands in registers, reach 6.5 PFLOP/s
-// here (zeros: 9.7): the power limit. A tile's stage is 2048 cycles of products for a SIMD's two
-// waves against about 1700 of LDS reads and 512 of LDS writes; without the stage loads the gate/up
-// kernel runs at 5.2 PFLOP/s, with them at 4.0 (65536 rows, 52 experts, H 7168, Hp 2048: 950
-// us), down with its 0.94 GB of output at 3.1 (620 us). With 384 experts (170 rows each) the weights' HBM
-// stream bounds it: gate/up 1.54 ms, 3.9 TB/s; down 0.87 ms, 4.5 TB/s.
-// Tried and slower (gate/up, 52 experts): stages of 128 with four in LDS, 64-byte requests (1039 us);
-// four waves of 128 x 128, a third less LDS traffic but one wave a SIMD and all 512 registers
-// (1109); touching the next stage's weight lines to bring them into L2 (989, and 1644 for 384 experts);
-// the next tile's first two stages before the stores (973, beside 968). No difference: wave priorities, CUs started half a tile
-// apart.
+// here (zeros: 9.7): the power limit. Gate/up of 65536 rows, 52 experts, H 7168, Hp 2048 takes 945-985
+// us (3.9-4.1 PFLOP/s; it varies from card to card), down with its 0.94 GB of output 620 (3.1). The
+// same gate/up work takes 780 us when all codes are zero, and without its epilogue then exactly as long as its
+// loads alone (731; the LDS reads alone 323): the load path is the second bound. With random codes products
+// and LDS reads without the loads take 740. With 384 experts (170 rows each) the weights' HBM stream bounds
+// it: gate/up 1.54 ms, 3.9 TB/s; down 0.87 ms, 4.5 TB/s.
+// Tried and not kept (gate/up, 52 experts, beside 968): stages of 128 with four in LDS, 64-byte requests
+// (1039 us); four waves of 128 x 128, a third less LDS traffic but one wave a SIMD and all 512
+// registers (1109); the next tile's first two stages before the stores (973). Touching the lines two or
+// three stages ahead, by one block per shared row or column panel and outside the stage's wait: no
+// change (down 620 -> 605, but 384 experts 1550 -> 1670 and 888 -> 922). No difference: wave priorities,
+// CUs started half a tile apart.
 #include "lds_dma.h"
 #include "mxfp4.h"
 #include "tile_sched.h"
