@@ -275,3 +275,21 @@ def test_ffn_mxfp4_nan_scale_stays_in_its_row():
     assert torch.isnan(y[:c.rows][hit]).all()
     assert torch.equal(h[0][:c.rows][rest], h0[0][:c.rows][rest])
     assert torch.equal(y[:c.rows][rest].view(torch.int16), y0[:c.rows][rest].view(torch.int16))
+
+
+@pytest.mark.parametrize("H,Hp", [(2048, 128), (1920, 256), (1152, 640), (128, 2304), (640, 1152)])
+def test_ffn_mxfp4_several_tiles_per_block(H, Hp):
+    """More tiles than CUs in one or both halves: a block goes on to its next tile while its stores are under
+    way, after whole and partial row blocks and after reductions of one, two and more stages."""
+    rng = np.random.default_rng(H)
+    counts = [int(c) for c in rng.integers(0, 300, 60)]
+    counts[:8] = [256, 32, 96, 128, 160, 255, 1, 0]
+    print(f"[case] rows {counts[:12]}.. H={H} Hp={Hp}", flush=True)
+    c = Case(counts, H, Hp, T=64, seed=Hp).gpu()
+    c.check()
+    h = c.gate_up()
+    y = c.down(*h)
+    for _ in range(3):
+        again = c.gate_up()
+        assert torch.equal(h[0], again[0]) and torch.equal(h[1], again[1])
+        assert torch.equal(y.view(torch.int16), c.down(*again).view(torch.int16))

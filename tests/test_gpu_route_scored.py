@@ -203,3 +203,21 @@ def test_unaligned_rows_and_buffers():
             tol = 192 * U + (2.0 ** -8 if dtype == "bf16" else 0) * np.abs(ref)
             assert (np.abs(g[1:-1].float().cpu().numpy().reshape(T, E) - ref) <= tol).all()
             assert g[0] == 5.0 and g[-1] == 5.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,K,G,tg", [(360, 15, 4, 1), (384, 16, 8, 1), (384, 32, 8, 2), (1023, 32, 33, 4), (1024, 16, 64, 1),
+                                      (1020, 30, 60, 2), (768, 32, 2, 1)])
+def test_few_kept_lanes_and_many_picks(E, K, G, tg, score, dtype):
+    """Few groups stay, whose lanes hold hardly more of the largest choices than there are picks."""
+    rng = np.random.default_rng(E + K)
+    lg = rng.standard_normal((150, E)).astype(np.float32)
+    lg[7] = np.sort(lg[7])             # a lane's experts far apart in rank, and all in one lane's reach
+    lg[8] = np.sort(lg[8])[::-1]
+    lg[9, ::2] = -np.inf
+    b = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    b[E // 2] = np.nan
+    for bias in (None, b):
+        check(lg, dtype, K, bias, score=score, groups=G, topk_groups=tg, group_top=2, renorm=True, scale=1.5)
+        check(lg, dtype, K, bias, score=score, groups=G, topk_groups=tg, group_top=1, renorm=False)
