@@ -300,7 +300,7 @@ MOE_API moe_status_t moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* sf, i
  *  layout MOE_MXFP4: q [E, N, K/2] out, or MOE_MXFP4_PAIRED: q [E, N/2, K/128, 2, 64] out
  *  (K % 128 == 0 and N % 2 == 0), bitwise what moe_pack_mxfp4_pairs makes of the former;
  *  sf [E, K/32, N] out in both. w and q 16-byte aligned, K % 32 == 0, K < 2^24 - 256,
- *  N <= 2^30, E <= 65535. */
+ *  N <= 2^30, K * N < 2^38, E <= 65535. */
 MOE_API moe_status_t moe_quantize_mxfp4_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K,
                                                 int32_t N, moe_dtype_t layout, uint8_t* q, uint8_t* sf,
                                                 hipStream_t stream);

@@ -377,6 +377,7 @@ static moe_status_t check_mxfp4_weights(moe_dtype_t dt, moe_dtype_t layout, int 
   if (dt != MOE_BF16 && dt != MOE_F32) return MOE_EUNSUPPORTED;
   if (layout != MOE_MXFP4 && layout != MOE_MXFP4_PAIRED) return MOE_EUNSUPPORTED;
   if (K % 32 || E > 65535 || K / 256 >= 65535 || N > 1 << 30) return MOE_EUNSUPPORTED;
+  if ((int64_t)K * N >= 1ll << 38) return MOE_EUNSUPPORTED;  // a thread per 128 values, counted in 32 bits
   if (layout == MOE_MXFP4_PAIRED && (K % 128 || N % 2)) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }

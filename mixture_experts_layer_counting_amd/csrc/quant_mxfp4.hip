@@ -11,10 +11,11 @@
 //            of one block: the block's maximum and codes need no other lane. A wave is 8 column
 //            groups x 8 k-blocks: each load instruction reads eight whole 128-byte lines, each
 //            store writes eight 128-byte runs of codes, without a pass through LDS.
-// All four are bound by HBM (a large copy reaches 4.9 TB/s here): rows 8192 x 7168 bf16 28 us, 5.3 TB/s, and
-// back 23 us; weights 52 x 7168 x 2048 bf16 376 us, 5.1 TB/s, and back 356 us; 64 x 2048 x 1024 fp32 134 us, 4.5
-// TB/s, and back to bf16 62 us.
+// All four are bound by HBM (a large copy reaches 4.9 TB/s here): rows 8192 x 7168 bf16 29 us, 5.1 TB/s, and
+// back 23 us; weights 52 x 7168 x 2048 bf16 385 us, 5.0 TB/s, and back 335 us; 64 x 2048 x 1024 fp32 136 us, 4.5
+// TB/s, and back to bf16 66 us. Rows that do not end on whole lines: see the kernels.
 #include "mxfp4.h"
+#include "tile_sched.h"
 
 namespace moe {
 
@@ -106,14 +107,31 @@ __device__ __forceinline__ size_t code_at(int n, int kb, int K) {
   return (size_t)n * (K / 2) + kb;
 }
 
+// Block x of a matrix's nx * ny blocks -> column block bx and k block by, in row order of the k blocks. With
+// `near`, column neighbours run on one XCD: where rows do not end on whole lines, two blocks share the
+// line at their border, and its parts meet in one L2.
+__device__ __forceinline__ void weight_block(int x, int blocks, int nx, bool near, int& bx, int& by) {
+  const int even = blocks & ~7;
+  const int at = near && x < even ? xcd_slot(x, even) : x;
+  by = at / nx;
+  bx = at - by * nx;
+}
+
+template <typename XT>
+__host__ __device__ __forceinline__ bool whole_lines(int N) {
+  return (size_t)N * sizeof(XT) % 128 == 0;
+}
+
 // Column groups of a matrix whose last group overlaps the one before where COLS does not divide N (the shared
 // columns are computed and written twice, alike). COLS = 1: fewer columns than a group.
 template <typename XT, int COLS, bool PAIRED>
-__global__ __launch_bounds__(256) void quant_weights_kernel(const XT* __restrict__ w, int K, int N,
+__global__ __launch_bounds__(256) void quant_weights_kernel(const XT* __restrict__ w, int K, int N, int nx,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cg = (blockIdx.x * 4 + wave) * 8 + (lane & 7);
-  const int kb = blockIdx.y * 8 + (lane >> 3);
+  int bx, by;  // in dispatch order whole lines are 2 % faster: 26 x 7168 x 2048 bf16 175 us, near 178
+  weight_block(blockIdx.x, gridDim.x, nx, !whole_lines<XT>(N), bx, by);
+  const int cg = (bx * 4 + wave) * 8 + (lane & 7);
+  const int kb = by * 8 + (lane >> 3);
   const int e = blockIdx.z;
   if (cg * COLS >= N || kb * 32 >= K) return;
   const int n0 = min(cg * COLS, N - COLS);
@@ -167,15 +185,20 @@ __global__ __launch_bounds__(256) void quant_weights_kernel(const XT* __restrict
   __builtin_memcpy(sf + ((size_t)e * (K / 32) + kb) * N + n0, pack, COLS);
 }
 
-// The way back: the same lane layout, codes read in 16-byte runs per column, rows written in
-// runs of COLS values.
-template <typename XT, int COLS, bool PAIRED>
+// The way back: codes read in 16-byte runs per column, rows written in runs of COLS values. A wave is CW column
+// groups x 64 / CW k-blocks: the wider, the fewer lines of the output it shares with a neighbour.
+// 26 x 7168 x N, us, CW 8 in dispatch order / 8, 16, 32 with near blocks:
+//   bf16  N 2048: 196 / 193, 185, 192   N 2046: 295 / 269, 230, 220   N 1001: 142 / 126, 112, 110
+//   fp32  N 2048: 321 / 328, 332, 333   N 2046: 589 / 519, 429, 387   N 1001: 282 / 250, 211, 190
+template <typename XT, int COLS, bool PAIRED, int CW>
 __global__ __launch_bounds__(256) void dequant_weights_kernel(const uint8_t* __restrict__ q,
-                                                              const uint8_t* __restrict__ sf, int K, int N,
+                                                              const uint8_t* __restrict__ sf, int K, int N, int nx,
                                                               XT* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int cg = (blockIdx.x * 4 + wave) * 8 + (lane & 7);
-  const int kb = blockIdx.y * 8 + (lane >> 3);
+  int bx, by;
+  weight_block(blockIdx.x, gridDim.x, nx, true, bx, by);
+  const int cg = (bx * 4 + wave) * CW + lane % CW;
+  const int kb = by * (64 / CW) + lane / CW;
   const int e = blockIdx.z;
   if (cg * COLS >= N || kb * 32 >= K) return;
   const int n0 = min(cg * COLS, N - COLS);
@@ -217,10 +240,20 @@ __global__ __launch_bounds__(256) void dequant_weights_kernel(const uint8_t* __r
   }
 }
 
-template <typename XT, int COLS>
-dim3 weight_grid(int E, int K, int N) {
+// Blocks of CW column groups per wave x 64 / CW k-blocks: nx of them along the columns, the matrix's in x.
+template <int COLS, int CW>
+dim3 weight_grid(int E, int K, int N, int& nx) {
   const int groups = (N + COLS - 1) / COLS;
-  return dim3((groups + 31) / 32, (K / 32 + 7) / 8, E);
+  nx = (groups + 4 * CW - 1) / (4 * CW);
+  const unsigned ny = (K / 32 + 64 / CW - 1) / (64 / CW);
+  return dim3((unsigned)nx * ny, 1, E);
+}
+
+template <typename XT, bool PAIRED, int COLS>
+void quant_weights_cols(const XT* w, int E, int K, int N, uint8_t* q, uint8_t* sf, hipStream_t s) {
+  int nx;
+  const dim3 grid = weight_grid<COLS, 8>(E, K, N, nx);
+  quant_weights_kernel<XT, COLS, PAIRED><<<grid, 256, 0, s>>>(w, K, N, nx, q, sf);
 }
 
 template <typename XT, bool PAIRED>
@@ -228,19 +261,28 @@ void quant_weights(const void* w, int E, int K, int N, uint8_t* q, uint8_t* sf, 
   constexpr int COLS = 16 / sizeof(XT);
   const XT* src = static_cast<const XT*>(w);
   if (N >= COLS)
-    quant_weights_kernel<XT, COLS, PAIRED><<<weight_grid<XT, COLS>(E, K, N), 256, 0, s>>>(src, K, N, q, sf);
+    quant_weights_cols<XT, PAIRED, COLS>(src, E, K, N, q, sf, s);
   else
-    quant_weights_kernel<XT, 1, PAIRED><<<weight_grid<XT, 1>(E, K, N), 256, 0, s>>>(src, K, N, q, sf);
+    quant_weights_cols<XT, PAIRED, 1>(src, E, K, N, q, sf, s);
+}
+
+template <typename XT, bool PAIRED, int COLS, int CW>
+void dequant_weights_cols(const uint8_t* q, const uint8_t* sf, int E, int K, int N, XT* out, hipStream_t s) {
+  int nx;
+  const dim3 grid = weight_grid<COLS, CW>(E, K, N, nx);
+  dequant_weights_kernel<XT, COLS, PAIRED, CW><<<grid, 256, 0, s>>>(q, sf, K, N, nx, out);
 }
 
 template <typename XT, bool PAIRED>
 void dequant_weights(const uint8_t* q, const uint8_t* sf, int E, int K, int N, void* out, hipStream_t s) {
   constexpr int COLS = 16 / sizeof(XT);
   XT* dst = static_cast<XT*>(out);
-  if (N >= COLS)
-    dequant_weights_kernel<XT, COLS, PAIRED><<<weight_grid<XT, COLS>(E, K, N), 256, 0, s>>>(q, sf, K, N, dst);
+  if (N < COLS)
+    dequant_weights_cols<XT, PAIRED, 1, 8>(q, sf, E, K, N, dst, s);
+  else if (whole_lines<XT>(N))
+    dequant_weights_cols<XT, PAIRED, COLS, 16>(q, sf, E, K, N, dst, s);
   else
-    dequant_weights_kernel<XT, 1, PAIRED><<<weight_grid<XT, 1>(E, K, N), 256, 0, s>>>(q, sf, K, N, dst);
+    dequant_weights_cols<XT, PAIRED, COLS, 32>(q, sf, E, K, N, dst, s);
 }
 
 }  // namespace

@@ -122,3 +122,9 @@ def test_sizes_past_one_launch_are_refused():
     for n in (2 ** 30 + 2, 2 ** 31 - 2):                         # column numbers past 32 bits in a lane
         assert status(moe.moe_quantize_mxfp4_weights, P, moe.MOE_BF16, 1, 128, n, moe.MOE_MXFP4, P, P, 0) == UNSUP
         assert status(moe.moe_dequantize_mxfp4_weights, P, P, moe.MOE_MXFP4_PAIRED, 1, 128, n, P, moe.MOE_F32, 0) == UNSUP
+
+
+def test_matrices_past_one_launch_are_refused():
+    for k, n in ((2 ** 8, 2 ** 30), (2 ** 20, 2 ** 18), (2 ** 23, 2 ** 30)):  # 2^38 values and more in one matrix
+        assert status(moe.moe_quantize_mxfp4_weights, P, moe.MOE_F32, 1, k, n, moe.MOE_MXFP4, P, P, 0) == UNSUP
+        assert status(moe.moe_dequantize_mxfp4_weights, P, P, moe.MOE_MXFP4, 1, k, n, P, moe.MOE_F32, 0) == UNSUP

@@ -293,3 +293,11 @@ def test_ffn_mxfp4_several_tiles_per_block(H, Hp):
         again = c.gate_up()
         assert torch.equal(h[0], again[0]) and torch.equal(h[1], again[1])
         assert torch.equal(y.view(torch.int16), c.down(*again).view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,K,N", [(3, 384, 1030), (2, 2176, 514), (1, 128, 4102), (2, 896, 1022), (5, 128, 2048), (1, 160, 2047),
+                                   (9, 1152, 8)])
+def test_quantize_weights_in_many_blocks(E, K, N, dtype):
+    """Matrices of several blocks along either axis, rows that end on whole lines and rows that do not."""
+    test_quantize_weights_and_back(E, K, N, dtype)
