@@ -452,7 +452,8 @@ MOE_API moe_status_t moe_grouped_ffn_fused_scatter(const void* x, moe_dtype_t ac
  * accumulated in fp32; h is rounded to MXFP4 once, from its fp32 value, in blocks of 32 columns
  * (arithmetic as moe_quantize_mxfp4).
  *  x_q [T, H/2], x_sf [T, H/32] from moe_quantize_mxfp4, read through row_src [M] (row r is
- *  token row_src[r] / K; -1: a padding row, zeros), or, with row_src NULL, [M, H/2] and
+ *  token row_src[r] / K; -1: a padding row, whose h is zeros, codes and scale bytes, whatever the
+ *  weights hold; down takes it like any other row), or, with row_src NULL, [M, H/2] and
  *  [M, H/32] rows in group order (T and K are then not used);
  *  w_gate, w_up [E, Hp, H/2], w_down [E, H, Hp/2], scales sf_gate, sf_up [E, H/32, Hp] and
  *  sf_down [E, Hp/32, H] in the MOE_MXFP4 layout (not the paired one);

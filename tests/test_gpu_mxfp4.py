@@ -301,3 +301,34 @@ def test_ffn_mxfp4_several_tiles_per_block(H, Hp):
 def test_quantize_weights_in_many_blocks(E, K, N, dtype):
     """Matrices of several blocks along either axis, rows that end on whole lines and rows that do not."""
     test_quantize_weights_and_back(E, K, N, dtype)
+
+
+@pytest.mark.parametrize("counts,H,Hp", [([3, 5, 0, 2], 256, 128), ([40, 300, 0, 130], 384, 256), ([100, 20], 128, 128)])
+def test_ffn_mxfp4_padding_rows_beside_nan_weights(counts, H, Hp):
+    """A weight block that holds NaN (scale byte 255) reaches every row of its expert, but not the padding rows:
+    their h is zeros in both kernels (few rows: streamed, many: tiles)."""
+    rows = sum(counts)
+    pad = tuple(range(1, rows, 3))
+    c = Case(counts, H, Hp, pad=pad, seed=rows)
+    clean = Case(counts, H, Hp, pad=pad, seed=rows).gpu()
+    for w, s in ((c.wg, c.sg), (c.wu, c.su)):
+        s[0, 1, 70] = 255
+        w[0, 70, 16:32] = 0
+    c.sg[1, 2, 33] = 255
+    c.wg[1, 33, 32:48] = 0
+    c.gpu()
+    h, h0 = c.gate_up(), clean.gate_up()
+    src = torch.from_numpy(c.src[:rows]).to(DEV)
+    for q, sf in (h, h0):
+        assert not q[:rows][src < 0].any() and not sf[:rows][src < 0].any()
+    expert = torch.from_numpy(np.repeat(np.arange(len(counts)), counts)).to(DEV)
+    live = src >= 0
+    blocks = {0: [70 // 32], 1: [33 // 32]}
+    for e in range(len(counts)):
+        at = (expert == e) & live
+        for b in range(Hp // 32):
+            if b in blocks.get(e, ()):
+                assert (h[1][:rows][at][:, b] == 255).all()
+            else:
+                assert torch.equal(h[1][:rows][at][:, b], h0[1][:rows][at][:, b])
+    assert not torch.isnan(c.down(*h)[:rows][~live].float()).any()
