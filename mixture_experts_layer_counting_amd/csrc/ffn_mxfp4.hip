@@ -439,8 +439,10 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
 // the second. In a step of 512 a lane takes the 64 bytes at 64 G of its column, two whole lines
 // per column and step, and the next step's loads are out before this one's products. A block
 // of eight waves takes 32 columns of gate and of up, each split in two along the reduction, and adds and rounds
-// through LDS (one block of the format is 32 columns), or 128 columns of down. Blocks walk the
-// experts that have rows.
+// through LDS (one block of the format is 32 columns), or 128 columns of down. An expert with more
+// rows than that gets a block per 16 RG of them: one after the other in one block, an uneven batch
+// would wait for its largest expert (gate/up, H 7168, Hp 128, 2048 rows all on one of 64 experts: 1413 us, side
+// by side 26, as long as the same rows spread evenly; 128 rows on one of 8, Hp 2048: 184, 26).
 
 constexpr int S4_THREADS = 512;
 
@@ -453,26 +455,38 @@ struct S4Step {
 template <bool GATED, int RG>
 __global__ __launch_bounds__(S4_THREADS) void ffn_mxfp4_stream_kernel(Mx4Args a) {
   constexpr int BN = GATED ? 32 : 128;  // columns of a block
+  constexpr int ROWS = 16 * RG;
   __shared__ float part[GATED ? 8 : 1][GATED ? RG : 1][16][17];  // [wave][row group][row][column]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = a.N, kb = a.Kd / 2, ksf = a.Kd / 32;
   const int ncb = N / BN;
-  const int idx = xcd_slot(blockIdx.x, gridDim.x);
-  const int cb = idx % ncb;
-  int left = idx / ncb, e = -1;
-  for (int base = 0; base < a.E; base += 64) {  // the left-th expert that has rows
-    const int i = base + lane;
-    const uint64_t m = __ballot(i < a.E && a.cu[min(i, a.E - 1) + 1] > a.cu[min(i, a.E - 1)]);
-    const int n = __popcll(m);
-    if (left < n) {
-      const uint64_t hit = __ballot(((m >> lane) & 1) && popc_below(m) == left);
-      e = base + __builtin_ctzll(hit);
+  // Eight neighbours on one XCD (they share scale lines, a heavy expert's also panels), the eights round-robin:
+  // the blocks without a chunk are the last ones and leave every XCD the same work (8 experts, 16 rows each: 35 us;
+  // with the whole range cut into eight, 49).
+  const int whole = gridDim.x & ~63;
+  const int b = blockIdx.x;
+  const int idx = b < whole ? (b & ~63) + (b & 7) * 8 + ((b >> 3) & 7) : b;
+  const int left = idx / ncb;  // this block's chunk among the experts' chunks of ROWS rows, in expert order
+  int e = -1, before = 0, chunks = 0;
+  for (int base = 0; base < a.E; base += 64) {
+    const int i = min(base + lane, a.E - 1);
+    const int n = base + lane < a.E ? (a.cu[i + 1] - a.cu[i] + ROWS - 1) / ROWS : 0;
+    int upto = popc_below(__ballot(n > 0)) + n;
+    if (__ballot(n > 1)) upto = sched_wave_incl_scan(n);
+    const uint64_t hit = __ballot(before + upto > left);
+    if (hit) {
+      const int j = __builtin_ctzll(hit);
+      e = base + j;
+      chunks = __builtin_amdgcn_readlane(n, j);
+      before += __builtin_amdgcn_readlane(upto, j) - chunks;
       break;
     }
-    left -= n;
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
   if (e < 0) return;
+  const int local = idx - before * ncb;
+  const int cb = local / chunks, r0 = (local - cb * chunks) * ROWS;
   const int gbeg = __builtin_amdgcn_readfirstlane(a.cu[e]);
   const int rows = __builtin_amdgcn_readfirstlane(a.cu[e + 1]) - gbeg;
 
@@ -485,117 +499,114 @@ __global__ __launch_bounds__(S4_THREADS) void ffn_mxfp4_stream_kernel(Mx4Args a)
   const int first = GATED && wave >= 4 ? (steps + 1) / 2 : 0;
   const int last = GATED && wave < 4 ? (steps + 1) / 2 : steps;
 
-  for (int r0 = 0; r0 < rows; r0 += 16 * RG) {
-    const uint8_t *xp[RG], *xsp[RG];
-    int nrg = 0;
+  const uint8_t *xp[RG], *xsp[RG];
+  int nrg = 0;
 #pragma unroll
-    for (int g = 0; g < RG; ++g) {
-      // rows past the last read it again; their results are not stored
-      int r = gbeg + min(r0 + 16 * g + c16, rows - 1);
-      if (GATED && a.row_src) {
-        const int src = a.row_src[r];
-        r = src < 0 ? 0 : min(src / a.a_k, a.a_rows - 1);
-      }
-      xp[g] = a.A + (size_t)r * kb + G * 64;
-      xsp[g] = a.A_sf + (size_t)r * ksf + 4 * G;
-      nrg += r0 + 16 * g < rows;
+  for (int g = 0; g < RG; ++g) {
+    // rows past the last read it again; their results are not stored
+    int r = gbeg + min(r0 + 16 * g + c16, rows - 1);
+    if (GATED && a.row_src) {
+      const int src = a.row_src[r];
+      r = src < 0 ? 0 : min(src / a.a_k, a.a_rows - 1);
     }
-    f32x4_t acc[RG];
+    xp[g] = a.A + (size_t)r * kb + G * 64;
+    xsp[g] = a.A_sf + (size_t)r * ksf + 4 * G;
+    nrg += r0 + 16 * g < rows;
+  }
+  f32x4_t acc[RG];
 #pragma unroll
-    for (int g = 0; g < RG; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // Step `it` of this lane; past the end of the reduction (a last step that is not whole) zeros.
-    auto load = [&](S4Step<RG>& d, int it) __attribute__((always_inline)) {
-      const bool in = it * 256 + G * 64 < kb;
-      const int o = in ? it * 256 : 0, os = in ? it * 16 : 0;
+  for (int g = 0; g < RG; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // Step `it` of this lane; past the end of the reduction (a last step that is not whole) zeros.
+  auto load = [&](S4Step<RG>& d, int it) __attribute__((always_inline)) {
+    const bool in = it * 256 + G * 64 < kb;
+    const int o = in ? it * 256 : 0, os = in ? it * 16 : 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) d.w[q] = *reinterpret_cast<const i32x4_t*>(wp + (in ? o : -G * 64) + 16 * q);
+    for (int q = 0; q < 4; ++q) d.w[q] = *reinterpret_cast<const i32x4_t*>(wp + (in ? o : -G * 64) + 16 * q);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) d.ws[q] = wsp[(ptrdiff_t)(in ? os + q : -4 * G) * N];
+    for (int q = 0; q < 4; ++q) d.ws[q] = wsp[(ptrdiff_t)(in ? os + q : -4 * G) * N];
+#pragma unroll
+    for (int g = 0; g < RG; ++g)
+      if (g < nrg) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d.x[g][q] = *reinterpret_cast<const i32x4_t*>(xp[g] + (in ? o : -G * 64) + 16 * q);
+        d.xs[g] = *reinterpret_cast<const int*>(xsp[g] + (in ? os : -4 * G));
+      }
+    if (!in) {
+      const i32x4_t z = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        d.w[q] = z;
+        d.ws[q] = 0;
+      }
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d.x[g][q] = z;
+        d.xs[g] = 0;
+      }
+    }
+  };
+  auto mul = [&](const S4Step<RG>& d) __attribute__((always_inline)) {
+    const i32x4_t z = {0, 0, 0, 0};
+    auto one = [&](auto q_) __attribute__((always_inline)) {
+      constexpr int q = decltype(q_)::value;
+      const i32x8_t wf = __builtin_shufflevector(d.w[q], z, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
       for (int g = 0; g < RG; ++g)
         if (g < nrg) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) d.x[g][q] = *reinterpret_cast<const i32x4_t*>(xp[g] + (in ? o : -G * 64) + 16 * q);
-          d.xs[g] = *reinterpret_cast<const int*>(xsp[g] + (in ? os : -4 * G));
+          const i32x8_t xf = __builtin_shufflevector(d.x[g][q], z, 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[g], 4, 4, 0, d.ws[q], q, d.xs[g]);
         }
-      if (!in) {
-        const i32x4_t z = {0, 0, 0, 0};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          d.w[q] = z;
-          d.ws[q] = 0;
-        }
-#pragma unroll
-        for (int g = 0; g < RG; ++g) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) d.x[g][q] = z;
-          d.xs[g] = 0;
-        }
-      }
     };
-    auto mul = [&](const S4Step<RG>& d) __attribute__((always_inline)) {
-      const i32x4_t z = {0, 0, 0, 0};
-      auto one = [&](auto q_) __attribute__((always_inline)) {
-        constexpr int q = decltype(q_)::value;
-        const i32x8_t wf = __builtin_shufflevector(d.w[q], z, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int g = 0; g < RG; ++g)
-          if (g < nrg) {
-            const i32x8_t xf = __builtin_shufflevector(d.x[g][q], z, 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[g] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[g], 4, 4, 0, d.ws[q], q, d.xs[g]);
-          }
-      };
-      one(std::integral_constant<int, 0>{});
-      one(std::integral_constant<int, 1>{});
-      one(std::integral_constant<int, 2>{});
-      one(std::integral_constant<int, 3>{});
-    };
-    S4Step<RG> s0, s1;
-    if (first < last) load(s0, first);
-    for (int it = first; it < last; it += 2) {
-      if (it + 1 < last) load(s1, it + 1);
-      mul(s0);
-      if (it + 2 < last) load(s0, it + 2);
-      if (it + 1 < last) mul(s1);
-    }
+    one(std::integral_constant<int, 0>{});
+    one(std::integral_constant<int, 1>{});
+    one(std::integral_constant<int, 2>{});
+    one(std::integral_constant<int, 3>{});
+  };
+  S4Step<RG> s0, s1;
+  if (first < last) load(s0, first);
+  for (int it = first; it < last; it += 2) {
+    if (it + 1 < last) load(s1, it + 1);
+    mul(s0);
+    if (it + 2 < last) load(s0, it + 2);
+    if (it + 1 < last) mul(s1);
+  }
 
-    // lane l holds row l % 16 of its group, columns 4G..4G+3 of the wave's 16
-    if constexpr (GATED) {
-      __syncthreads();  // the previous row chunk's sums are read
+  // lane l holds row l % 16 of its group, columns 4G..4G+3 of the wave's 16
+  if constexpr (GATED) {
 #pragma unroll
-      for (int g = 0; g < RG; ++g)
+    for (int g = 0; g < RG; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][g][c16][4 * G + i] = acc[g][i];
-      __syncthreads();
-      // wave g rounds row group g: lane = 4 row + quarter of the 32 columns
-      const int r = lane >> 2, j = lane & 3;
-      if (wave < RG && r0 + 16 * wave + r < rows) {
-        const int row = gbeg + r0 + 16 * wave + r;
-        const bool pad = a.row_src && a.row_src[row] < 0;
-        float v[8];
-        uint32_t m = 0;
+      for (int i = 0; i < 4; ++i) part[wave][g][c16][4 * G + i] = acc[g][i];
+    __syncthreads();
+    // wave g rounds row group g: lane = 4 row + quarter of the 32 columns
+    const int r = lane >> 2, j = lane & 3;
+    if (wave < RG && r0 + 16 * wave + r < rows) {
+      const int row = gbeg + r0 + 16 * wave + r;
+      const bool pad = a.row_src && a.row_src[row] < 0;
+      float v[8];
+      uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int hw = j >> 1, c = (j & 1) * 8 + i;
-          const float gate = part[hw][wave][r][c] + part[4 + hw][wave][r][c];
-          const float up = part[2 + hw][wave][r][c] + part[6 + hw][wave][r][c];
-          v[i] = pad ? 0.f : silu_f32(gate) * up;
-          m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        }
-        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
-        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
-        const uint32_t byte = mx_scale_byte(m);
-        *reinterpret_cast<uint32_t*>(a.h_q + (size_t)row * (N / 2) + cb * 16 + 4 * j) = mx_pack8(v, byte);
-        if (j == 0) a.h_sf[(size_t)row * (N / 32) + cb] = (uint8_t)byte;
+      for (int i = 0; i < 8; ++i) {
+        const int hw = j >> 1, c = (j & 1) * 8 + i;
+        const float gate = part[hw][wave][r][c] + part[4 + hw][wave][r][c];
+        const float up = part[2 + hw][wave][r][c] + part[6 + hw][wave][r][c];
+        v[i] = pad ? 0.f : silu_f32(gate) * up;
+        m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
       }
-    } else {
+      m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0xB1, 0xF, 0xF, false));
+      m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x4E, 0xF, 0xF, false));
+      const uint32_t byte = mx_scale_byte(m);
+      *reinterpret_cast<uint32_t*>(a.h_q + (size_t)row * (N / 2) + cb * 16 + 4 * j) = mx_pack8(v, byte);
+      if (j == 0) a.h_sf[(size_t)row * (N / 32) + cb] = (uint8_t)byte;
+    }
+  } else {
 #pragma unroll
-      for (int g = 0; g < RG; ++g) {
-        const int r = r0 + 16 * g + c16;
-        if (r < rows)
-          *reinterpret_cast<uint2*>(a.y + (size_t)(gbeg + r) * N + n0 + 4 * G) =
-              make_uint2(pack_bf16x2(acc[g][0], acc[g][1]), pack_bf16x2(acc[g][2], acc[g][3]));
-      }
+    for (int g = 0; g < RG; ++g) {
+      const int r = r0 + 16 * g + c16;
+      if (r < rows)
+        *reinterpret_cast<uint2*>(a.y + (size_t)(gbeg + r) * N + n0 + 4 * G) =
+            make_uint2(pack_bf16x2(acc[g][0], acc[g][1]), pack_bf16x2(acc[g][2], acc[g][3]));
     }
   }
 }
@@ -603,12 +614,15 @@ __global__ __launch_bounds__(S4_THREADS) void ffn_mxfp4_stream_kernel(Mx4Args a)
 template <bool GATED>
 moe_status_t launch_stream(const Mx4Args& a, int M, hipStream_t s) {
   const int slots = M < a.E ? M : a.E;  // at most so many experts have rows
-  const int64_t grid = (int64_t)slots * (a.N / (GATED ? 32 : 128));
   // (two groups of 16 rows a pass cost more than one where most experts have fewer than eight)
-  if (M <= 8 * slots)
-    ffn_mxfp4_stream_kernel<GATED, 1><<<(unsigned)grid, S4_THREADS, 0, s>>>(a);
+  const int rg = M <= 8 * slots ? 1 : 2;
+  // n experts with R rows make at most n + (R - n) / (16 rg) chunks; blocks past the last one have none
+  const int64_t chunks = slots + (M - slots) / (16 * rg);
+  const unsigned grid = (unsigned)(chunks * (a.N / (GATED ? 32 : 128)));
+  if (rg == 1)
+    ffn_mxfp4_stream_kernel<GATED, 1><<<grid, S4_THREADS, 0, s>>>(a);
   else
-    ffn_mxfp4_stream_kernel<GATED, 2><<<(unsigned)grid, S4_THREADS, 0, s>>>(a);
+    ffn_mxfp4_stream_kernel<GATED, 2><<<grid, S4_THREADS, 0, s>>>(a);
   return launch_status();
 }
 

@@ -332,3 +332,67 @@ def test_ffn_mxfp4_padding_rows_beside_nan_weights(counts, H, Hp):
             else:
                 assert torch.equal(h[1][:rows][at][:, b], h0[1][:rows][at][:, b])
     assert not torch.isnan(c.down(*h)[:rows][~live].float()).any()
+
+
+# Uneven small batches, which stream in both halves: experts with several chunks of 16 rows (at most 8 rows per
+# expert on average) or of 32 (more).
+UNEVEN = [
+    ([70, 0, 1, 0, 17, 0, 0, 3, 0, 0, 0, 0], 384, 128, (2, 69, 80)),
+    ([100, 0, 33, 32, 1, 0, 0, 0, 0, 0, 0, 0], 512, 128, (0, 31, 99, 131)),
+    ([0] * 7 + [64], 640, 256, ()),
+    ([0] * 7 + [120], 1152, 128, (64, 65)),
+    ([0, 0, 0, 40] + [0] * 60 + [1, 16, 17] + [0] * 80 + [50, 0, 0], 256, 128, (41, 123)),
+]
+
+
+@pytest.mark.parametrize("counts,H,Hp,pad", UNEVEN, ids=lambda s: "_".join(map(str, s[:5])) if isinstance(s, (list, tuple)) else str(s))
+def test_ffn_mxfp4_uneven_small_batches(counts, H, Hp, pad):
+    print(f"[case] rows {counts[:12]}.. H={H} Hp={Hp}", flush=True)
+    Case(counts, H, Hp, pad=pad, seed=len(counts)).gpu().check()
+
+
+@pytest.mark.parametrize("counts", [[9, 0, 3, 1], [0, 50, 3, 0, 0, 0]])
+def test_ffn_mxfp4_nan_scale_stays_in_its_row_streamed(counts):
+    rows = sum(counts)
+    c = Case(counts, 384, 128, seed=4)
+    clean = Case(counts, 384, 128, seed=4).gpu()
+    t = int(c.src[5]) // c.K
+    c.x_sf[t, 7] = 255
+    c.x_q[t, 7 * 16:8 * 16] = 0
+    c.gpu()
+    h, h0 = c.gate_up(), clean.gate_up()
+    y, y0 = c.down(*h), clean.down(*h0)
+    hit = torch.from_numpy(c.src[:rows] // c.K == t).to(DEV)
+    assert (h[1][:rows][hit] == 255).all() and torch.isnan(y[:rows][hit]).all()
+    assert torch.equal(h[0][:rows][~hit], h0[0][:rows][~hit]) and torch.equal(h[1][:rows][~hit], h0[1][:rows][~hit])
+    assert torch.equal(y[:rows][~hit].view(torch.int16), y0[:rows][~hit].view(torch.int16))
+
+
+def median_us(call, calls=5, times=7):
+    call()
+    got = []
+    for _ in range(times):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(calls):
+            call()
+        b.record()
+        torch.cuda.synchronize()
+        got.append(a.elapsed_time(b) * 1e3 / calls)
+    return sorted(got)[times // 2]
+
+
+def test_ffn_mxfp4_a_heavy_expert_does_not_serialise_a_small_batch():
+    """2048 rows on one of 64 experts read one expert's weights, not 64: they may not take many times the evenly
+    spread batch's time (one block per column panel took 54 times)."""
+    H, Hp, E, M = 7168, 128, 64, 2048
+    us = []
+    for counts in ([M // E] * E, [0] * 40 + [M] + [0] * (E - 41)):
+        c = Case(counts, H, Hp, T=M, K=1, tail=0).gpu()
+        d = c.d
+        h_q = torch.empty(M, Hp // 2, dtype=torch.uint8, device=DEV)
+        h_sf = torch.empty(M, Hp // 32, dtype=torch.uint8, device=DEV)
+        us.append(median_us(lambda: moe.moe_ffn_gate_up_mxfp4(d["x_q"], d["x_sf"], d["src"], M, 1, d["cu"], M, E, H, Hp, d["wg"],
+                                                              d["wu"], d["sg"], d["su"], h_q, h_sf)))
+    print(f"[time] even {us[0]:.1f} us, one expert {us[1]:.1f} us", flush=True)
+    assert us[1] <= 6 * us[0]
