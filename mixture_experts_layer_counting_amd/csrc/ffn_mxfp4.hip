@@ -629,20 +629,28 @@ moe_status_t launch_stream(const Mx4Args& a, int M, hipStream_t s) {
 // Whether the streaming kernel takes M rows over E experts and N columns. It does where the tiles
 // could not fill the chip: up to `slots` experts have rows, each with N / bn tiles. Measured on 256
 // CUs, us, streamed against tiles, rows per expert in brackets:
-//   gate/up  8 experts, H 7168, Hp 2048 (128 tiles): [4] 27 / 39  [16] 34 / 39  [32] 48 / 39
-//            16 experts, the same (256 tiles): [1] 54 / 53;  42 experts (672): [1.5] 161 / 142
-//            4 experts, H 2560, Hp 1280 (40 tiles): [16] 8.0 / 15.8  [32] 10.9 / 15.5  [48] 16.5 / 16.3
-//   down     8 experts, Hp 2048, H 7168 (224 tiles): [1] 14.9 / 16.4  [4] 15.8 / 14.6  [16] 20 / 15
-//            4 experts, Hp 1280, H 2560 (40 tiles): [16] 8.2 / 9.8  [32] 11.4 / 10.1
-// Gate/up streams up to 16 rows per expert while the tiles do not outnumber the CUs and up to 32 while they are
-// a quarter of them; down, whose reduction is short, up to 2 and 16.
+//   gate/up  8 experts, H 7168, Hp 2048 (128 tiles): [4] 25 / 38  [16] 34 / 38  [24] 44 / 38
+//            12 experts, the same (192 tiles): [1] 31 / 38  [8] 38 / 38  [16] 50 / 39
+//            16 experts, the same (256 tiles): [1] 39 / 39  [4] 43 / 39  [16] 66 / 39
+//            24 experts, H 1024, Hp 1024 (192 tiles): [1] 8.6 / 9.8  [8] 9.4 / 9.9  [16] 12.8 / 9.8
+//            4 experts, H 2560, Hp 1280 (40 tiles): [16] 8.4 / 15.8  [32] 11.1 / 16.1  [48] 19.7 / 16.6
+//            all rows on one of 8 experts (128 tiles): [4] 18 / 29  [16] 27 / 32  [32] 50 / 45
+//            1000 rows on one of 256 experts, 12 on the others, Hp 128 (256 tiles): 77 / 75
+//   down     8 experts, Hp 2048, H 7168 (224 tiles): [1] 13.3 / 15.9  [4] 14.7 / 15.8  [16] 21 / 16
+//            128 experts, Hp 128, H 7168 (3584 tiles): [1] 40 / 35
+//            4 experts, Hp 1280, H 2560 (40 tiles): [16] 8.9 / 10.1  [32] 11.5 / 10.9
+//            all rows on one of 16 experts, Hp 2048, H 1024 (64 tiles): [8] 11.0 / 11.8  [16] 15.5 / 15.9
+// Gate/up streams up to 32, 16 and 8 rows per expert while the tiles are a quarter, a half and three quarters of
+// the CUs; down, whose reduction is short, up to 16 and 2 while they are a quarter and all of them.
 bool streams(bool gated, int M, int E, int N) {
   const int slots = M < E ? M : E;
   const int bn = gated ? M4_BN / 2 : M4_BN;
   const int64_t tiles = (int64_t)slots * ((N + bn - 1) / bn);
   const int cus = device_cu_count();
-  const int64_t few = gated ? 16 : 2, more = gated ? 32 : 16;
-  return (M <= few * slots && tiles <= cus) || (M <= more * slots && 4 * tiles <= cus);
+  if (gated)
+    return (M <= 32 * slots && 4 * tiles <= cus) || (M <= 16 * slots && 2 * tiles <= cus) ||
+           (M <= 8 * slots && 4 * tiles <= 3 * cus);
+  return (M <= 16 * slots && 4 * tiles <= cus) || (M <= 2 * slots && tiles <= cus);
 }
 
 template <bool GATED>

@@ -396,3 +396,20 @@ def test_ffn_mxfp4_a_heavy_expert_does_not_serialise_a_small_batch():
                                                               d["wu"], d["sg"], d["su"], h_q, h_sf)))
     print(f"[time] even {us[0]:.1f} us, one expert {us[1]:.1f} us", flush=True)
     assert us[1] <= 6 * us[0]
+
+
+@pytest.mark.parametrize("E,Hp", [(256, 128), (16, 2048)])
+def test_ffn_mxfp4_fewer_rows_do_not_take_longer(E, Hp):
+    """As many tiles as CUs, 16 and 17 rows per expert: whichever kernel takes them, one row less per expert may not
+    cost more (streamed, the 16 took 1.6 times the 17's time)."""
+    H, us = 7168, []
+    for r in (16, 17):
+        M = E * r
+        c = Case([r] * E, H, Hp, T=M, K=1, tail=0).gpu()
+        d = c.d
+        h_q = torch.empty(M, Hp // 2, dtype=torch.uint8, device=DEV)
+        h_sf = torch.empty(M, Hp // 32, dtype=torch.uint8, device=DEV)
+        us.append(median_us(lambda: moe.moe_ffn_gate_up_mxfp4(d["x_q"], d["x_sf"], d["src"], M, 1, d["cu"], M, E, H, Hp, d["wg"],
+                                                              d["wu"], d["sg"], d["su"], h_q, h_sf)))
+    print(f"[time] 16 rows {us[0]:.1f} us, 17 rows {us[1]:.1f} us", flush=True)
+    assert us[0] <= 1.25 * us[1]
