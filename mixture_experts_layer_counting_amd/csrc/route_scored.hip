@@ -79,9 +79,9 @@ __device__ __forceinline__ const void* logit_row(const ScoredArgs& a, int t) {
   return static_cast<const char*>(a.logits) + (size_t)t * a.E * (a.bf16 ? 2 : 4);
 }
 
-// The fp32 choices of one lane's experts, -inf where masked (or NaN by a NaN bias: like -inf it is greater
-// than nothing). top, total: the softmax's largest
-// logit and sum. (The branches are uniform and outside the loops: each loop is straight code.)
+// The fp32 choices of one lane's experts, -inf where masked, by the logit or by a bias of -inf or NaN (a NaN
+// must not go on: fmed3 may return it, and as an integer key it would be the largest). top, total: the softmax's
+// largest logit and sum. (The branches are uniform and outside the loops: each loop is straight code.)
 template <int ITEMS>
 __device__ __forceinline__ void choices(const ScoredArgs& a, bool scores, const float (&l)[ITEMS],
                                         const float (&bias)[ITEMS], float top, float total, float (&s)[ITEMS],
@@ -101,7 +101,7 @@ __device__ __forceinline__ void choices(const ScoredArgs& a, bool scores, const 
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     c[i] = with_bias ? s[i] + bias[i] : l[i];
-    if (!(l[i] > NEG_INF)) c[i] = NEG_INF;
+    if (!(l[i] > NEG_INF && c[i] > NEG_INF)) c[i] = NEG_INF;
   }
 }
 

@@ -221,3 +221,18 @@ def test_few_kept_lanes_and_many_picks(E, K, G, tg, score, dtype):
     for bias in (None, b):
         check(lg, dtype, K, bias, score=score, groups=G, topk_groups=tg, group_top=2, renorm=True, scale=1.5)
         check(lg, dtype, K, bias, score=score, groups=G, topk_groups=tg, group_top=1, renorm=False)
+
+
+@pytest.mark.parametrize("E,K", [(65, 3), (130, 16), (384, 8), (1000, 32)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_and_infinite_biases(E, K, dtype):
+    """Experts that only a bias of NaN or -inf masks, in lanes that hold several, without groups and with them."""
+    rng = np.random.default_rng(E)
+    lg = rng.standard_normal((40, E)).astype(np.float32)
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    b[rng.random(E) < 0.3] = np.nan
+    b[rng.random(E) < 0.2] = -np.inf
+    for score in ("sigmoid", "softmax"):
+        check(lg, dtype, K, b, score=score, renorm=True)
+        check(lg, dtype, K, np.where(np.arange(E) < E - K + 1, np.float32(np.nan), b), score=score, renorm=False)
+        check(lg, dtype, K, b, score=score, renorm=True, groups=5 if E % 5 == 0 else 3, topk_groups=2 + (K > 16), group_top=2)
