@@ -9,7 +9,7 @@
 //   picks:  the K largest c (equal: lower id);  w_k = scale * s_k [/ sum over the picks]
 // The choices are compared as if in binary64. One wave takes one token with its logits in
 // registers. It computes the choices in fp32, whose error the bounds below limit; only where two
-// neighbouring picks (or two group scores) lie closer than twice that error does the wave redo
+// neighbouring picks (or two group scores) lie within their own bound does the wave redo
 // the choice in fp64. Everything else needs no 64-bit arithmetic, and the result is the fp64 one
 // in every case. Reading the logits once is the whole memory traffic.
 //
@@ -25,6 +25,7 @@ namespace {
 constexpr float NEG_INF = -__builtin_inff();
 constexpr int RS_WAVES = 4;
 constexpr int RS_MAX_E = 1024;
+constexpr float HUGE_CHOICE = 1e30f;  // past this a sum of choices or a bound may overflow in fp32
 // Eight waves a SIMD where the logits leave the registers for it.
 #define RS_OCCUPANCY(items) __attribute__((amdgpu_waves_per_eu((items) <= 8 ? 8 : 1)))
 
@@ -149,10 +150,16 @@ __device__ __forceinline__ void top_two(F u, F& m1, F& m2) {
   m1 = u > m1 ? u : m1;
 }
 
-// Whether this lane's group stays, from its lanes' two largest choices. tol > 0: `close` is set where
-// a kept and a dropped group's scores differ by no more than 2 tol.
+// How far a choice of value v has to lie from another for their order in fp32 to be the exact one.
+struct Bound {
+  float base, slope;
+  __device__ __forceinline__ float at(float v) const { return base + slope * __builtin_fabsf(v); }
+};
+
+// Whether this lane's group stays, from its lanes' two largest choices. In fp32, with a bound > 0, `close` is set
+// (for the whole wave) where a kept and a dropped group's scores may be ordered the other way.
 template <typename F>
-__device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, F tol, F m1, F m2, bool& close) {
+__device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, Bound bound, F m1, F m2, bool& close) {
   const F ninf = (F)NEG_INF;
   const int g = lane >> a.lp;
   auto merge = [&](F o1, F o2) {
@@ -166,18 +173,27 @@ __device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, F tol,
   if (a.lp >= 3) merge(pair_lane<4>(m1), pair_lane<4>(m2));
   if (a.lp >= 4) merge(pair_lane<8>(m1), pair_lane<8>(m2));
   if (a.lp >= 5) merge(pair_lane<16>(m1), pair_lane<16>(m2));
-  const F score = a.group_top == 2 && m2 > ninf ? m1 + m2 : m1;
+  const bool both = a.group_top == 2 && m2 > ninf;
+  const F score = both ? m1 + m2 : m1;
   int rank = 0;
-  F under = ninf;  // the largest score that comes after this one
   for (int j = 0; j < a.G; ++j) {
     const F o = lane_value(score, j << a.lp);
     const bool before = j < g ? o >= score : o > score;
     rank += before ? 1 : 0;
-    if (tol > 0) under = !before && j != g && o > under ? o : under;
   }
   const bool kept = g < a.G && rank < a.topk_groups;
-  // only the border matters: the last kept group and the one after it
-  if (tol > 0) close = rank == a.topk_groups - 1 && g < a.G && score > ninf && score - under <= 2 * tol;
+  if constexpr (sizeof(F) == 4) {
+    if (bound.base > 0.f) {
+      // Each of the two largest choices errs by at most a quarter of its bound, their sum by 2^-24 of it: the
+      // score stays within `wide` of the exact one, with room for the roundings here. (A sum of huge negative
+      // choices that overflows is -inf: two such count as close. Huge positive ones go the plain way.)
+      const bool live = g < a.G && m1 > ninf;
+      const float wide = 0.5f * (bound.at(m1) + bound.at(both ? m2 : m1));
+      const float dropped = wave_max(live && !kept ? score + wide : NEG_INF);
+      const float least = -wave_max(live && kept ? wide - score : NEG_INF);
+      close = dropped >= least;
+    }
+  }
   return kept;
 }
 
@@ -210,7 +226,7 @@ __device__ __forceinline__ int choose_exact(ScoredArgs a, const float* row, floa
 #pragma unroll 1
     for (int i = 0; i < items; ++i) top_two(choice(i, a.group_top == 2), m1, m2);
     bool close = false;
-    kept = group_kept<double>(a, lane, 0.0, m1, m2, close);
+    kept = group_kept<double>(a, lane, Bound{0.f, 0.f}, m1, m2, close);
   }
   uint32_t taken = 0;
   int my_e = -1;
@@ -330,21 +346,15 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
   choices<ITEMS>(a, scores, l, bias, top, total, s, c);
   // How far apart two choices are surely ordered alike in fp32 and exactly. exp errs by
   // (2 |x| + 2) 2^-24 of its value. Sigmoid: s (1 - s) |x| <= 0.23, so s errs by less than 1.5 *
-  // 2^-22, and rounding c by 2^-24 |c|; twice that is below 2^-20 (1 + |c|). Softmax: the sum
-  // over up to 1024 experts adds at most 2^-18.2, relative to the largest score, 1 / total. Both
-  // get a factor of two on top. Without scores the choices are the logits: exact.
-  float tol = 0.f;
-  if (scores) {
-    float big = 0.f;
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-        if (c[i] > NEG_INF) big = fmaxf(big, __builtin_fabsf(c[i]));
-      big = wave_max(big);
-    }
-    tol = a.sigmoid ? 0x1p-19f * (1.0f + big) : 0x1p-16f / total + 0x1p-20f * big;
-  }
-  bool close = false;
+  // 2^-22, and rounding c by 2^-24 |c|: below 2^-21 (1 + |c|). Softmax: the sum over up to 1024
+  // experts adds at most 2^-18.2, relative to the largest score, 1 / total. The bound is four times
+  // a choice's error e(c). Two choices c > d may be ordered the other way only if c - d <= e(c) + e(d), and e grows
+  // with |c| so slowly that e(d) <= e(c) + 2^-19 (c - d): then c - d is below the bound at c (and at d). So each
+  // choice counts with its own size: an expert switched off by a bias of -1e9 does not widen the others' bound.
+  // Without scores the choices are the logits: exact.
+  Bound bound{0.f, 0.f};
+  if (scores) bound = a.sigmoid ? Bound{0x1p-19f, 0x1p-19f} : Bound{0x1p-16f / total, 0x1p-20f};
+  bool plain = false;  // an infinite or huge choice
   if (a.G > 1) {
     const bool use_s = a.group_top == 2 && !a.bias;
     float m1 = NEG_INF, m2 = NEG_INF;
@@ -354,28 +364,28 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
       m2 = __builtin_amdgcn_fmed3f(u, m1, m2);  // the second of the three, m1 >= m2
       m1 = u > m1 ? u : m1;
     }
-    bool kept = group_kept<float>(a, lane, tol, m1, m2, close);
-    if (__ballot(close)) {
+    plain = a.bias && __ballot(m1 > HUGE_CHOICE) != 0;
+    bool close = false;
+    bool kept = group_kept<float>(a, lane, bound, m1, m2, close);
+    if (close) {
       const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
       double d1 = (double)NEG_INF, d2 = d1;
       // a lane's two largest in fp64 are among those within the bound of its second in fp32
-      const float low = a.bias ? m2 - 2.0f * tol : m2;
+      const float low = m2 - 2.0f * bound.at(m2);
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
-        const bool in = c[i] > NEG_INF && (use_s ? s[i] >= low - 2.0f * tol : c[i] >= low);
+        const bool in = c[i] > NEG_INF && (use_s ? s[i] : c[i]) >= low;
         if (__ballot(in)) {
           const double d = exact_score(a, l[i], top, sum) + (double)bias[i];
           if (in) top_two(d, d1, d2);
         }
       }
-      kept = group_kept<double>(a, lane, 0.0, d1, d2, close);
+      kept = group_kept<double>(a, lane, bound, d1, d2, close);
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
       if (!kept) c[i] = NEG_INF;
   }
-  bool plain = !(tol < 1e30f);  // an infinite or huge bias
-  const float gap = a.bias ? tol : 0.f;
 
   float best = NEG_INF, second = NEG_INF;
 #pragma unroll
@@ -383,6 +393,7 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
     second = __builtin_amdgcn_fmed3f(c[i], best, second);
     best = c[i] > best ? c[i] : best;
   }
+  if (a.bias && a.G == 1) plain = __ballot(best > HUGE_CHOICE) != 0;
   const int none = order_key(NEG_INF);
   int own = order_key(best), next = order_key(second), key = none;
   for (int k = 0; k < a.K; ++k) {
@@ -391,7 +402,8 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
     own = taken ? next : own;
     next = taken ? none : next;
   }
-  const float bar = key_value(key) - gap;
+  const float last = key_value(key);
+  const float bar = a.bias ? last - bound.at(last) : last;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
@@ -428,8 +440,9 @@ __global__ __launch_bounds__(64 * RS_WAVES) RS_OCCUPANCY(ITEMS) void route_score
       // the neighbours in rank, through LDS
       if (lane < n) cand[wave][rank].x = v;
       wave_sync();
+      const float here = lane < n ? cand[wave][lane].x : NEG_INF;
       const float after = lane + 1 < n ? cand[wave][lane + 1].x : NEG_INF;
-      if (__ballot(lane + 1 < n && cand[wave][lane].x - after <= gap)) {
+      if (__ballot(lane + 1 < n && here - after <= bound.at(here))) {
         const float lv = lane < n ? mine[e] : 0.f;
         const double sum = a.sigmoid ? 1.0 : exact_total<ITEMS>(l, top);
         const double x = lane < n ? exact_score(a, lv, top, sum) + (double)a.bias[e] : (double)NEG_INF;

@@ -236,3 +236,59 @@ def test_nan_and_infinite_biases(E, K, dtype):
         check(lg, dtype, K, b, score=score, renorm=True)
         check(lg, dtype, K, np.where(np.arange(E) < E - K + 1, np.float32(np.nan), b), score=score, renorm=False)
         check(lg, dtype, K, b, score=score, renorm=True, groups=5 if E % 5 == 0 else 3, topk_groups=2 + (K > 16), group_top=2)
+
+
+LOW = float(np.finfo(np.float32).min)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,K,G,tg", [(384, 8, 8, 4), (384, 8, 1, 1), (96, 6, 4, 2), (1024, 32, 16, 5), (60, 4, 6, 3)])
+def test_experts_switched_off_or_forced_by_finite_biases(E, K, G, tg, score):
+    """Large finite biases on some experts, on a whole group, and both ways: the order of the others, and of those that
+    only differ below the large biases' fp32 steps, is the exact one."""
+    rng = np.random.default_rng(E + G)
+    lg = rng.standard_normal((24, E)).astype(np.float32)
+    lg[5] = np.round(lg[5])                       # equal and near choices
+    lg[6] = 0.5
+    S = E // G
+    for big in (-1e4, -1e9, -1e30, LOW, 1e6, 1e9, 1e29, 1e31):
+        for at in (rng.choice(E, 5, replace=False), np.arange(S), np.concatenate([np.arange(0, E, S), [1, 2]]),
+                   rng.choice(E, E - K // 2, replace=False)):
+            b = (rng.standard_normal(E) * 0.05).astype(np.float32)
+            b[at] = big
+            b[at[0]] = np.nextafter(np.float32(big), np.float32(0))
+            for top in (1, 2):
+                check(lg, "f32", K, b, backward=False, score=score, groups=G, topk_groups=tg, group_top=top, renorm=True)
+    b = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    b[::7], b[1::7], b[2::7] = -1e9, LOW, np.nan
+    b[3], b[S % E] = 1e9, 1e9
+    check(lg, "f32", K, b, backward=False, score=score, groups=G, topk_groups=tg, group_top=2, renorm=False)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,tg,top", [(1, 1, 1), (8, 4, 2), (8, 4, 1)])
+def test_a_few_large_biases_do_not_slow_the_batch(G, tg, top, score):
+    """Five experts switched off, or two forced, by large finite biases: the other experts' order needs no more
+    arithmetic than before (with one bound for all of them the batch took 7 times as long)."""
+    T, E, K = 8192, 384, 8
+    rng = np.random.default_rng(0)
+    lg = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(DEV)
+    idx, w = torch.empty(T, K, dtype=torch.int32, device=DEV), torch.empty(T, K, device=DEV)
+    d = desc(T, E, K, score=score, groups=G, topk_groups=tg, group_top=top)
+    us = {}
+    for big, n in ((0, 0), (-1e9, 5), (-1e30, 5), (LOW, 5), (1e9, 2)):
+        b = torch.from_numpy(rng.standard_normal(E).astype(np.float32) * (0.1 if score == "sigmoid" else 0.001)).to(DEV)
+        if n:
+            b[torch.arange(n) * (E // n) + 3] = big
+        got = []
+        for _ in range(7):
+            s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            s.record()
+            for _ in range(20):
+                moe.moe_route_scored(d, lg, moe.MOE_F32, b, idx, w)
+            e.record()
+            torch.cuda.synchronize()
+            got.append(s.elapsed_time(e) * 1e3 / 20)
+        us[big] = sorted(got)[3]
+    print(f"[time] {us}", flush=True)
+    assert max(us.values()) <= 3 * us[0]
