@@ -376,8 +376,10 @@ static moe_status_t check_mxfp4_weights(moe_dtype_t dt, moe_dtype_t layout, int 
   if (E < 0 || K < 0 || N < 0) return MOE_EINVAL;
   if (dt != MOE_BF16 && dt != MOE_F32) return MOE_EUNSUPPORTED;
   if (layout != MOE_MXFP4 && layout != MOE_MXFP4_PAIRED) return MOE_EUNSUPPORTED;
+  // A launch's threads along x are counted in 32 bits: one per 128 values, and whole blocks of up to 1024 columns x 64 k. A
+  // narrow matrix leaves most of a block empty, 256 threads per 64 k however few its columns: K is bounded by itself too.
   if (K % 32 || E > 65535 || K / 256 >= 65535 || N > 1 << 30) return MOE_EUNSUPPORTED;
-  if ((int64_t)K * N >= 1ll << 38) return MOE_EUNSUPPORTED;  // a thread per 128 values, counted in 32 bits
+  if ((int64_t)K * N >= 1ll << 38) return MOE_EUNSUPPORTED;
   if (layout == MOE_MXFP4_PAIRED && (K % 128 || N % 2)) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }

@@ -592,6 +592,13 @@ moe_status_t launch_route_scored(const moe_route_desc_t& d, const void* logits, 
                                  int* topk_idx, float* topk_w, hipStream_t s) {
   if (d.T == 0) return MOE_OK;
   const ScoredArgs a = scored_args(d, logits, lt, bias);
+  // A lane holds `items` experts; the kernel is built for the powers of two and for 6, and an empty slot costs what
+  // a full one does. 8192 tokens, 8 picks, bias, sigmoid, us, a form against the next larger one (without groups; 8 groups):
+  //   64 experts   1 /  2:  6.3 /  6.7;   8.4 /  9.0      384 experts   6 /  8:  8.6 /  9.5;  11.4 / 12.6
+  //   128          2 /  4:  7.1 /  7.9;   9.1 / 10.2      512           8 / 16:  9.6 / 14.2;  12.6 / 18.0
+  //   256          4 /  6:  8.0 /  8.6;  11.0 / 11.9      1024         16 / 32: 14.4 / 30.4;  21.6 / 41.0
+  // From 16 on the logits no longer leave the registers for eight waves a SIMD. 32 serves groups that fill their
+  // lanes badly (33 groups of 31: one lane each).
   const int items = (a.S + (1 << a.lp) - 1) >> a.lp;
   const dim3 grid((a.T + RS_WAVES - 1) / RS_WAVES), block(64 * RS_WAVES);
   if (items <= 1)
