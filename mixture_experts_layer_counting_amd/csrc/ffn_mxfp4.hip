@@ -129,7 +129,6 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     int e, row0, rows_valid, n0, nmt;
     i32x4_t rA, rS, rB0, rB1;
     int a_off[M4_LD], s_off;
-    uint64_t pad[MT];  // lanes whose row of block mt is a padding row
   };
   auto decode = [&](int t) __attribute__((always_inline)) {
     Tile d;
@@ -155,12 +154,7 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
       for (int i = 0; i < M4_LD; ++i)
         d.a_off[i] = (ld_row[i] < d.rows_valid && src[i] >= 0) ? (src[i] / a.a_k) * kb + ld_chunk * 16 : M4_OUT;
       d.s_off = (sa_row < d.rows_valid && ssrc >= 0) ? (ssrc / a.a_k) * ksf + sa_half * 16 : M4_OUT;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        d.pad[mt] = __ballot(a.row_src[d.row0 + min(mt * 128 + wm * 32 + (lane & 31), d.rows_valid - 1)] < 0);
     } else {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) d.pad[mt] = 0;
       d.rA = make_rsrc(a.A + (size_t)d.row0 * kb, (uint32_t)d.rows_valid * (uint32_t)kb);
       d.rS = make_rsrc(a.A_sf + (size_t)d.row0 * ksf, (uint32_t)d.rows_valid * (uint32_t)ksf);
 #pragma unroll
@@ -357,7 +351,6 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
     else k_loop(std::integral_constant<int, 0>{});
 
     const int row0 = cur.row0, rows_valid = cur.rows_valid, n0 = cur.n0, nmt = cur.nmt;
-    const uint64_t pads[MT] = {cur.pad[0], cur.pad[1]};
     // The next tile's first stage goes into the buffer that stage nk - 1 did not use, whose readers all
     // passed the last barrier. So do those of the row scales' other half.
     if (t + G < total) {
@@ -394,17 +387,19 @@ __global__ __launch_bounds__(M4_THREADS, 1) void ffn_mxfp4_kernel(Mx4Args a) {
             for (int i = 0; i < 16; ++i) {
               const int at = 8 * p + i / 2;  // 4j + c, two columns each
               v[i] = silu_f32(acc[0][mt][i & 1][at]) * acc[1][mt][i & 1][at];
+              m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
             }
-            // zeros by definition: its zero codes times a weight block whose scale is NaN are NaN
-            if (pads[mt] != 0) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if ((pads[mt] >> lane) & 1) v[i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
             const auto both = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-            const uint32_t byte = mx_scale_byte(max((uint32_t)both[0], (uint32_t)both[1]));
+            uint32_t byte = mx_scale_byte(max((uint32_t)both[0], (uint32_t)both[1]));
+            // A padding row is zeros, but its zero codes times a weight block whose scale is NaN are NaN. Looked up
+            // only where a NaN came out, so that the tiles without one load nothing for it.
+            if (a.row_src && __ballot(byte == MX_NAN_SCALE) != 0) {
+              if (ok && byte == MX_NAN_SCALE && a.row_src[row] < 0) {
+                byte = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0.f;
+              }
+            }
             // the halves trade runs: group 0 gets columns 0..15 of the block, group 1 columns 16..31
             const auto tr = __builtin_amdgcn_permlane32_swap(mx_pack8(v, byte), mx_pack8(v + 8, byte), false, false);
             if (ok) {
