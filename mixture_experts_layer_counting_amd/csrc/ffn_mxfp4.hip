@@ -20,12 +20,13 @@
 // products of this one, across the stage barrier too.
 //
 // What bounds it. With random codes the matrix cores alone, operands in registers, reach 6.5 PFLOP/s
-// here (zeros: 9.7): the power limit. Gate/up of 65536 rows, 52 experts, H 7168, Hp 2048 takes 945-985
-// us (3.9-4.1 PFLOP/s; it varies from card to card), down with its 0.94 GB of output 620 (3.1). The
+// here (zeros: 9.7): the power limit. Gate/up of 65536 rows, 52 experts, H 7168, Hp 2048 takes 944-979
+// us (medians by events on three cards; 3.9-4.1 PFLOP/s) and 1022-1086 in profiler traces (3.5-3.8), down with its
+// 0.94 GB of output 626 (3.1) and 646-663. The
 // same gate/up work takes 780 us when all codes are zero, and without its epilogue then exactly as long as its
 // loads alone (731; the LDS reads alone 323): the load path is the second bound. With random codes products
 // and LDS reads without the loads take 740. With 384 experts (170 rows each) the weights' HBM stream bounds
-// it: gate/up 1.54 ms, 3.9 TB/s; down 0.87 ms, 4.5 TB/s.
+// it: gate/up 1.53-1.55 ms (3.9 TB/s; traces 1.60), down 0.88-0.89 (4.4 TB/s; traces 0.94).
 // Tried and not kept (gate/up, 52 experts, beside 968): stages of 128 with four in LDS, 64-byte requests
 // (1039 us); four waves of 128 x 128, a third less LDS traffic but one wave a SIMD and all 512
 // registers (1109); the next tile's first two stages before the stores (973). Touching the lines two or
