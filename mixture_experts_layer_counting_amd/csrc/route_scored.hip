@@ -174,7 +174,9 @@ __device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, Bound 
   if (a.lp >= 4) merge(pair_lane<8>(m1), pair_lane<8>(m2));
   if (a.lp >= 5) merge(pair_lane<16>(m1), pair_lane<16>(m2));
   const bool both = a.group_top == 2 && m2 > ninf;
-  const F score = both ? m1 + m2 : m1;
+  F score = both ? m1 + m2 : m1;
+  // a sum of huge negative choices stays above a group that has none
+  if constexpr (sizeof(F) == 4) score = both ? fmaxf(score, -3.40282347e38f) : score;
   int rank = 0;
   for (int j = 0; j < a.G; ++j) {
     const F o = lane_value(score, j << a.lp);
@@ -185,8 +187,8 @@ __device__ __forceinline__ bool group_kept(const ScoredArgs& a, int lane, Bound 
   if constexpr (sizeof(F) == 4) {
     if (bound.base > 0.f) {
       // Each of the two largest choices errs by at most a quarter of its bound, their sum by 2^-24 of it: the
-      // score stays within `wide` of the exact one, with room for the roundings here. (A sum of huge negative
-      // choices that overflows is -inf: two such count as close. Huge positive ones go the plain way.)
+      // score stays within `wide` of the exact one, with room for the roundings here. (Two sums of huge negative
+      // choices that would overflow lie within `wide` of each other. Huge positive ones go the plain way.)
       const bool live = g < a.G && m1 > ninf;
       const float wide = 0.5f * (bound.at(m1) + bound.at(both ? m2 : m1));
       const float dropped = wave_max(live && !kept ? score + wide : NEG_INF);

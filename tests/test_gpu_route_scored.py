@@ -292,3 +292,23 @@ def test_a_few_large_biases_do_not_slow_the_batch(G, tg, top, score):
         us[big] = sorted(got)[3]
     print(f"[time] {us}", flush=True)
     assert max(us.values()) <= 3 * us[0]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,tg", [(12, 2, 1), (384, 8, 4), (10, 5, 4), (68, 34, 16), (462, 11, 8)])
+def test_a_group_of_lowest_biases_comes_before_one_with_nothing_left(E, G, tg, score):
+    """Groups whose two largest choices add up past the lowest fp32 value, beside groups that the logits or the bias
+    mask wholly: the former have experts to pick, however low."""
+    rng = np.random.default_rng(E)
+    S, K = E // G, min(32, tg * (E // G))
+    lg = rng.standard_normal((20, E)).astype(np.float32)
+    for t in range(10):                               # whole groups masked by the logits
+        for g in rng.choice(G, max(1, G // 3), replace=False):
+            lg[t, g * S:(g + 1) * S] = -np.inf
+    for none in (np.nan, -np.inf):
+        b = np.full(E, LOW, np.float32)
+        b[:S * (G // 2)] = none                       # the lower groups have nothing left
+        check(lg, "f32", K, b, backward=False, score=score, groups=G, topk_groups=tg, group_top=2, renorm=True)
+        b[S * (G - 1):] = rng.uniform(-3.4e38, 3.4e38, S)
+        b[S * (G // 2):S * (G // 2) + 1] = np.float32(-3.4e38)
+        check(lg, "f32", K, b, backward=False, score=score, groups=G, topk_groups=tg, group_top=2, renorm=False)
