@@ -488,6 +488,119 @@ MOE_API moe_status_t moe_grouped_ffn_mxfp4(const uint8_t* x_q, const uint8_t* x_
                                            const uint8_t* sf_down, void* y_rows, void* ws, size_t ws_bytes,
                                            hipStream_t stream);
 
+/* INT8: signed codes with one fp32 scale per row of activations or per output column of weights,
+ * value = code * scale. Symmetric, no zero point:
+ *     s = max(fl32(amax / 127), 2^-120), amax the largest magnitude of the row (column); 1 where it is 0,
+ *     q = x / s rounded to the nearest integer, ties to even, as if in infinite precision (|q| <= 127).
+ * A row with a NaN or an infinity gets scale NaN and zero codes, so that what is computed from it is NaN.
+ *
+ * Activations to INT8 ("Mixture of Kittens", Step 8: activations are quantised for the expert GEMMs):
+ *  x [R, C] of x_dtype (BF16 or F32), any C >= 1; q [R, C] codes out, sf [R] fp32 out. Pointers need
+ *  the alignment of their elements only. One kernel launch, HBM-bound. */
+MOE_API moe_status_t moe_quantize_int8(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t C, int8_t* q,
+                                       float* sf, hipStream_t stream);
+
+/* The values of moe_quantize_int8's output: out [R, C] = fl32(q * sf), rounded to out_dtype (BF16 or F32). */
+MOE_API moe_status_t moe_dequantize_int8(const int8_t* q, const float* sf, int32_t R, int32_t C, void* out,
+                                         moe_dtype_t out_dtype, hipStream_t stream);
+
+/* Stacked weights to INT8 with a scale per output column ("Mixture of Kittens", Step 8: the weights are
+ * pre-quantised once): w [E, K, N] of w_dtype (BF16 or F32), K the reduction: the layout of the bf16 and fp32
+ * experts; q [E, N, K] out (reduction-contiguous), sf [E, N] out. Any K and N with K * N < 2^40;
+ * alignment of the elements only. Two kernel launches. */
+MOE_API moe_status_t moe_quantize_int8_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K, int32_t N,
+                                               int8_t* q, float* sf, hipStream_t stream);
+
+/* The values of INT8 weights: out [E, K, N] = fl32(q * sf), rounded to out_dtype (BF16 or F32). */
+MOE_API moe_status_t moe_dequantize_int8_weights(const int8_t* q, const float* sf, int32_t E, int32_t K, int32_t N,
+                                                 void* out, moe_dtype_t out_dtype, hipStream_t stream);
+
+/* Dense product in INT8 with scales per token and per output column (a projection outside the experts,
+ * such as a shared expert's):
+ *     y[t, n] = (sum_k x_q[t, k] w_q[n, k]) * x_sf[t] * w_sf[n].
+ * The sum is exact (32-bit integers), converted to fp32, scaled by the row's and then the column's
+ * scale and rounded to `out` (BF16 or F32).
+ *  x_q [M, H] and x_sf [M] from moe_quantize_int8, w_q [N, H] and w_sf [N] from
+ *  moe_quantize_int8_weights (E = 1); y [M, N]. Codes may be any int8, -128 included. A row whose scale is
+ *  0 gives zeros.
+ * x_q and w_q 16-byte aligned, the others by their elements. Needs H % 16 == 0, H < 2^17 (the sum's range),
+ * N <= 2^20, M <= 2^30 and (M / 64 + 1) (N / 64 + 1) < 2^31 (MOE_EUNSUPPORTED). One kernel launch,
+ * deterministic. */
+MOE_API moe_status_t moe_matmul_int8(const int8_t* x_q, const float* x_sf, int32_t M, int32_t H, int32_t N,
+                                     const int8_t* w_q, const float* w_sf, void* y, moe_dtype_t out,
+                                     hipStream_t stream);
+
+/* The same product by expert group ("Distributed expert parallelism", "Grouped expert computation"): for
+ * the rows r in [cu_seqlens[e], cu_seqlens[e+1]) of expert e, with t = row_src[r] / K,
+ *     y[r, n] = (sum_k x_q[t, k] w_q[e, n, k]) * x_sf[t] * w_sf[e, n].
+ *  x_q [T, H], x_sf [T], read through row_src [M] from moe_permute (negative: a padding row, which gives
+ *  zeros whatever the weights hold; so does one whose token is not below T), or, with row_src NULL,
+ *  [M, H] and [M] in group order (T and K are then not used); w_q [E, N, H], w_sf [E, N]; y_rows [M, N] of
+ *  `out` (BF16 or F32). Rows outside the groups are not written. cu_seqlens is ascending within
+ *  [0, M]; entries outside are taken as the nearer end.
+ * Limits as moe_matmul_int8 with (M / 64 + E) (N / 64 + 1) < 2^31, E <= 1024 and T*H < 2^31. One kernel
+ * launch, deterministic. */
+MOE_API moe_status_t moe_grouped_matmul_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T,
+                                             int32_t K, const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H,
+                                             int32_t N, const int8_t* w_q, const float* w_sf, void* y_rows,
+                                             moe_dtype_t out, hipStream_t stream);
+
+/* First half of the expert FFN in INT8 ("Mixture of Kittens", Step 1, the SwiGLU expert; Step 8,
+ * low-precision expert GEMMs): for the rows of every expert
+ *     g = x . Wg[e],  u = x . Wu[e],  h[r] = silu(g) * u,
+ * both products as in moe_grouped_matmul_int8 (kept in fp32), h [M, Hp] bf16. w_gate, w_up [E, Hp, H], sf_gate,
+ * sf_up [E, Hp]; other arguments and limits as there, with N = Hp. One kernel launch. */
+MOE_API moe_status_t moe_ffn_gate_up_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T,
+                                          int32_t K, const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H,
+                                          int32_t Hp, const int8_t* w_gate, const int8_t* w_up, const float* sf_gate,
+                                          const float* sf_up, void* h, hipStream_t stream);
+
+/* Scratch bytes of moe_grouped_ffn_int8: h [M, Hp] bf16 at offset 0, its codes [M, Hp] and its scales [M]
+ * each at the next multiple of 256 (0 for invalid sizes). */
+MOE_API size_t moe_grouped_ffn_int8_workspace_bytes(int32_t M, int32_t Hp);
+
+/* The expert FFN in INT8: moe_ffn_gate_up_int8, h quantised per row (moe_quantize_int8), and the down product
+ * y_rows[r] = h[r] . Wd[e] (moe_grouped_matmul_int8; w_down [E, H, Hp], sf_down [E, H]), y_rows [M, H] bf16. h, its
+ * codes and scales live in `ws` (16-byte aligned); calls that share a workspace must be ordered. Needs the limits
+ * of both products (H % 16 == 0 and Hp % 16 == 0 among them). Three kernel launches. */
+MOE_API moe_status_t moe_grouped_ffn_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T,
+                                          int32_t K, const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H,
+                                          int32_t Hp, const int8_t* w_gate, const int8_t* w_up, const int8_t* w_down,
+                                          const float* sf_gate, const float* sf_up, const float* sf_down,
+                                          void* y_rows, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Product of every expert's rows with its own matrix ("Distributed expert parallelism", "Grouped expert
+ * computation"; MoonEP "Integration": stacked weights, cu_seqlens selecting each expert's rows), for
+ * experts that are not SwiGLU FFNs: adapters, single projections. For the rows r of expert e, with x_r row
+ * r of x, or row row_src[r] / K where row_src is given,
+ *     transposed = 0:  y_rows[r] = x_r . W[e],    W [E, H, N]
+ *     transposed = 1:  y_rows[r] = x_r . W[e]^T,  W [E, N, H]
+ * accumulated in fp32. Each is the other's data gradient: dx_rows = dy_rows . W[e]^T is the call with
+ * `transposed` changed, H and N exchanged, on the same W (and moe_combine without weights adds the rows
+ * of a token).
+ *  act = wgt: BF16 with out BF16 or F32, or F32 with out F32 (MOE_EUNSUPPORTED otherwise). x [M, H] in group
+ *  order, or x [T, H] with row_src [M] from moe_permute (negative: a padding row, reads zeros; so does
+ *  one whose token is not below T); y_rows [M, N]. Rows outside the groups are not written. cu_seqlens as in
+ *  moe_grouped_matmul_int8.
+ * Any H and N up to 2^20, pointers aligned to their elements; rows that are whole 16-byte words (H, N and the
+ * base pointers) run the faster kernels. E <= 1024, M <= 2^30, (M / 64 + E) (N / 64 + 1) < 2^31 and, gathered,
+ * T*H*bytes < 2^31 (MOE_EUNSUPPORTED). One kernel launch, deterministic. */
+MOE_API moe_status_t moe_grouped_matmul(const void* x, moe_dtype_t act, const int32_t* row_src, int32_t T, int32_t K,
+                                        const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H, int32_t N,
+                                        const void* w, moe_dtype_t wgt, int32_t transposed, void* y_rows,
+                                        moe_dtype_t out, hipStream_t stream);
+
+/* The gradient of moe_grouped_matmul's weights ("MoonEP API walkthrough", the weight gradient of the group
+ * GEMM): dw[e] = sum over the rows r of expert e of x[r]^T dy[r], [E, H, N], accumulated in fp32; zero for an
+ * expert without rows. For output-major weights [E, N, H] exchange x with dy and H with N.
+ *  x [M, H] and dy [M, N] of `dtype` (BF16 or F32) in group order; dw_dtype F32, or BF16 for BF16 operands.
+ *  accumulate = 1 (F32 only): dw[e] is added to, as gradients of several micro-batches are; 0: written.
+ * Limits and alignment as moe_grouped_matmul, E (H / 64 + 1) (N / 64 + 1) < 2^31. One kernel launch,
+ * deterministic. */
+MOE_API moe_status_t moe_grouped_matmul_wgrad(const void* x, const void* dy, moe_dtype_t dtype,
+                                              const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H, int32_t N,
+                                              void* dw, moe_dtype_t dw_dtype, int32_t accumulate, hipStream_t stream);
+
 /* Combine ("Distributed expert parallelism", lifecycle item 8 and "A four-rank example";
  * MoonEP "combine fwd"): out[t] = sum_{k=0..K-1} topk_w[t,k] * y_rows[pos[t,k]], summed in
  * fp32 in increasing k and rounded once to `out_dtype`; rows with pos < 0 are skipped.

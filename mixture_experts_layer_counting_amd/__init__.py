@@ -38,6 +38,10 @@ EXPORTS = ("moe_route_topk", "moe_route_scored", "moe_route_scored_backward", "m
            "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_quantize_mxfp4_weights",
            "moe_dequantize_mxfp4_weights", "moe_ffn_gate_up_mxfp4", "moe_ffn_down_mxfp4",
            "moe_grouped_ffn_mxfp4_workspace_bytes", "moe_grouped_ffn_mxfp4",
+           "moe_quantize_int8", "moe_dequantize_int8", "moe_quantize_int8_weights",
+           "moe_dequantize_int8_weights", "moe_matmul_int8", "moe_grouped_matmul_int8",
+           "moe_ffn_gate_up_int8", "moe_grouped_ffn_int8_workspace_bytes", "moe_grouped_ffn_int8",
+           "moe_grouped_matmul", "moe_grouped_matmul_wgrad",
            "moe_grouped_ffn_workspace_bytes", "moe_grouped_ffn",
            "moe_grouped_ffn_fused_workspace_bytes", "moe_grouped_ffn_fused",
            "moe_grouped_ffn_fused_scatter", "moe_combine",
@@ -123,6 +127,17 @@ _SIGS = {
     "moe_grouped_ffn_mxfp4_workspace_bytes": (_S, [_I, _I]),
     "moe_grouped_ffn_mxfp4": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S,
                                    _P]),
+    "moe_quantize_int8": (_I, [_P, _E, _I, _I, _P, _P, _P]),
+    "moe_dequantize_int8": (_I, [_P, _P, _I, _I, _P, _E, _P]),
+    "moe_quantize_int8_weights": (_I, [_P, _E, _I, _I, _I, _P, _P, _P]),
+    "moe_dequantize_int8_weights": (_I, [_P, _P, _I, _I, _I, _P, _E, _P]),
+    "moe_matmul_int8": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _E, _P]),
+    "moe_grouped_matmul_int8": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _E, _P]),
+    "moe_ffn_gate_up_int8": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_grouped_ffn_int8_workspace_bytes": (_S, [_I, _I]),
+    "moe_grouped_ffn_int8": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "moe_grouped_matmul": (_I, [_P, _E, _P, _I, _I, _P, _I, _I, _I, _I, _P, _E, _I, _P, _E, _P]),
+    "moe_grouped_matmul_wgrad": (_I, [_P, _P, _E, _P, _I, _I, _I, _I, _P, _E, _I, _P]),
     "moe_status_str": (ctypes.c_char_p, [_I]),
 }
 
@@ -299,6 +314,69 @@ def moe_grouped_ffn_mxfp4(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_g
                                        Hp, _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(sf_gate),
                                        _ptr(sf_up), _ptr(sf_down), _ptr(y_rows), _ptr(ws), ws_bytes,
                                        _stream(stream)), "moe_grouped_ffn_mxfp4")
+
+
+def moe_quantize_int8(x, x_dtype, R, C, q, sf, stream=None):
+    _check(lib().moe_quantize_int8(_ptr(x), x_dtype, R, C, _ptr(q), _ptr(sf), _stream(stream)),
+           "moe_quantize_int8")
+
+
+def moe_dequantize_int8(q, sf, R, C, out, out_dtype, stream=None):
+    _check(lib().moe_dequantize_int8(_ptr(q), _ptr(sf), R, C, _ptr(out), out_dtype, _stream(stream)),
+           "moe_dequantize_int8")
+
+
+def moe_quantize_int8_weights(w, w_dtype, E, K, N, q, sf, stream=None):
+    _check(lib().moe_quantize_int8_weights(_ptr(w), w_dtype, E, K, N, _ptr(q), _ptr(sf), _stream(stream)),
+           "moe_quantize_int8_weights")
+
+
+def moe_dequantize_int8_weights(q, sf, E, K, N, out, out_dtype, stream=None):
+    _check(lib().moe_dequantize_int8_weights(_ptr(q), _ptr(sf), E, K, N, _ptr(out), out_dtype,
+                                             _stream(stream)), "moe_dequantize_int8_weights")
+
+
+def moe_matmul_int8(x_q, x_sf, M, H, N, w_q, w_sf, y, out, stream=None):
+    _check(lib().moe_matmul_int8(_ptr(x_q), _ptr(x_sf), M, H, N, _ptr(w_q), _ptr(w_sf), _ptr(y), out,
+                                 _stream(stream)), "moe_matmul_int8")
+
+
+def moe_grouped_matmul_int8(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, N, w_q, w_sf, y_rows, out,
+                            stream=None):
+    _check(lib().moe_grouped_matmul_int8(_ptr(x_q), _ptr(x_sf), _ptr(row_src), T, K, _ptr(cu_seqlens), M, E, H,
+                                         N, _ptr(w_q), _ptr(w_sf), _ptr(y_rows), out, _stream(stream)),
+           "moe_grouped_matmul_int8")
+
+
+def moe_ffn_gate_up_int8(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up, h,
+                         stream=None):
+    _check(lib().moe_ffn_gate_up_int8(_ptr(x_q), _ptr(x_sf), _ptr(row_src), T, K, _ptr(cu_seqlens), M, E, H,
+                                      Hp, _ptr(w_gate), _ptr(w_up), _ptr(sf_gate), _ptr(sf_up), _ptr(h),
+                                      _stream(stream)), "moe_ffn_gate_up_int8")
+
+
+def moe_grouped_ffn_int8_workspace_bytes(M, Hp) -> int:
+    return int(lib().moe_grouped_ffn_int8_workspace_bytes(M, Hp))
+
+
+def moe_grouped_ffn_int8(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, w_down, sf_gate,
+                         sf_up, sf_down, y_rows, ws, ws_bytes, stream=None):
+    _check(lib().moe_grouped_ffn_int8(_ptr(x_q), _ptr(x_sf), _ptr(row_src), T, K, _ptr(cu_seqlens), M, E, H, Hp,
+                                      _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(sf_gate), _ptr(sf_up),
+                                      _ptr(sf_down), _ptr(y_rows), _ptr(ws), ws_bytes, _stream(stream)),
+           "moe_grouped_ffn_int8")
+
+
+def moe_grouped_matmul(x, act, row_src, T, K, cu_seqlens, M, E, H, N, w, wgt, transposed, y_rows, out,
+                       stream=None):
+    _check(lib().moe_grouped_matmul(_ptr(x), act, _ptr(row_src), T, K, _ptr(cu_seqlens), M, E, H, N, _ptr(w),
+                                    wgt, transposed, _ptr(y_rows), out, _stream(stream)),
+           "moe_grouped_matmul")
+
+
+def moe_grouped_matmul_wgrad(x, dy, dtype, cu_seqlens, M, E, H, N, dw, dw_dtype, accumulate, stream=None):
+    _check(lib().moe_grouped_matmul_wgrad(_ptr(x), _ptr(dy), dtype, _ptr(cu_seqlens), M, E, H, N, _ptr(dw),
+                                          dw_dtype, accumulate, _stream(stream)), "moe_grouped_matmul_wgrad")
 
 
 def moe_ffn_gate_up(x_perm, x_perm_sf, act, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up,

@@ -18,7 +18,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 
 SOURCES = ["route_topk.hip", "route_scored.hip", "permute.hip", "combine.hip", "quant.hip",
-           "quant_mxfp4.hip", "ffn_f32.hip", "ffn_mxfp4.hip",
+           "quant_mxfp4.hip", "quant_int8.hip", "matmul_int8.hip", "grouped_matmul.hip", "ffn_f32.hip", "ffn_mxfp4.hip",
            "ffn_bf16.hip", "ffn_fused.hip", "ffn_fp8.hip", "ffn_bwd.hip", "moe_api.cpp"]
 
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")

@@ -1,0 +1,405 @@
+// Products of ragged expert groups on gfx950's matrix cores: what the kernels of bf16, fp32 and INT8
+// share.
+//
+// Three products, C = A B per expert, all accumulated in 32 bits:
+//   rows x weights [K][N]     y[r, n]  = sum_k x[r, k] W[k, n]
+//   rows x weights [N][K]     y[r, n]  = sum_k x[r, k] W[n, k]
+//   rows^T x rows             dW[m, n] = sum_r x[r, m] dy[r, n]
+// An operand whose reduction runs along memory (KC) is staged as [rows][128 bytes], the other kind (MC)
+// as [k][columns]. One stage is 128 bytes of reduction per row of a KC operand: 64 bf16, 32 fp32 or 128
+// INT8 elements. In a step kk = 0..3 of a stage, lane l (half g = l / 32) feeds the matrix cores the 16 bytes of chunk 2 kk + g
+// of its row or column l % 32:
+//   bf16  v_mfma_f32_32x32x16_bf16, eight elements a lane: one instruction
+//   INT8  v_mfma_i32_32x32x32_i8, sixteen: one instruction
+//   fp32  v_mfma_f32_32x32x2_f32, one element a lane: four instructions, element j of each chunk
+// Which k a lane takes is free as long as both operands agree. The weights (B) are the first operand, so
+// a lane holds output row l % 32 and, in acc[4 j + c], column 8 j + 4 g + c.
+#pragma once
+
+#include "grouped_args.h"
+#include "lds_dma.h"
+#include "moe_common.h"
+#include "tile_sched.h"
+
+#include <type_traits>
+#include <utility>
+
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+namespace moe {
+
+constexpr int GG_MAX_E = 1024;
+
+// First row of group e, kept inside [0, M] whatever cu holds.
+__device__ __forceinline__ int group_begin(const int* cu, int e, int M) { return cu ? min(max(cu[e], 0), M) : e * M; }
+__device__ __forceinline__ int group_rows(const int* cu, int e, int M, int begin) {
+  return max(group_begin(cu, e + 1, M) - begin, 0);
+}
+
+// Writes tstart[0..E], the exclusive prefix of tiles(rows of e), and returns the total.
+template <int THREADS, typename F>
+__device__ int group_prefix(const int* cu, int M, int E, F tiles, int* tstart, int* wsum) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int total = 0;
+  for (int base = 0; base < E; base += THREADS) {
+    const int e = base + tid;
+    int c = 0;
+    if (e < E) c = tiles(group_rows(cu, e, M, group_begin(cu, e, M)));
+    const int incl = sched_wave_incl_scan(c);
+    if (lane == 63) wsum[wave] = incl;
+    __syncthreads();
+    int before = total;
+    for (int w = 0; w < THREADS / 64; ++w) {
+      if (w < wave) before += wsum[w];
+      total += wsum[w];
+    }
+    if (e < E) tstart[e] = before + incl - c;
+    __syncthreads();
+  }
+  if (tid == 0) tstart[E] = total;
+  __syncthreads();
+  return total;
+}
+
+// f(0), f(1), .. f(N - 1) with compile-time numbers.
+template <typename F, int... I>
+__device__ __forceinline__ void gg_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void gg_for(F&& f) {
+  gg_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// ---- element types ---------------------------------------------------------------------
+
+struct ElBf16 {
+  using mem_t = uint16_t;
+  using acc_t = f32x16_t;
+  static constexpr int BYTES = 2;
+  static __device__ __forceinline__ void mma(acc_t& acc, i32x4_t b, i32x4_t a) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, b), __builtin_bit_cast(bf16x8_t, a), acc,
+                                                  0, 0, 0);
+  }
+};
+
+struct ElI8 {
+  using mem_t = int8_t;
+  using acc_t = i32x16_t;
+  static constexpr int BYTES = 1;
+  static __device__ __forceinline__ void mma(acc_t& acc, i32x4_t b, i32x4_t a) {
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, acc, 0, 0, 0);
+  }
+};
+
+struct ElF32 {
+  using mem_t = float;
+  using acc_t = f32x16_t;
+  static constexpr int BYTES = 4;
+  static __device__ __forceinline__ void mma(acc_t& acc, i32x4_t b, i32x4_t a) {
+    const f32x4_t bf = __builtin_bit_cast(f32x4_t, b), af = __builtin_bit_cast(f32x4_t, a);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(bf[j], af[j], acc, 0, 0, 0);
+  }
+};
+
+// ---- staged operands -------------------------------------------------------------------
+// An operand of R rows (KC) or columns (MC) takes R * 128 bytes of LDS per stage, R * 8 chunks of 16.
+// Chunk c lies at byte 16 c and holds:
+//   KC  row c / 8, k chunk (c % 8) ^ (row / 2 % 8): sixteen lanes that read one chunk of sixteen rows
+//       hit all banks once
+//   MC  bf16: k row c / (R / 8), 32-byte segments swizzled by 2 (k % 4), for the transposing reads;
+//       fp32: k row c / (R / 4), in order
+template <class EL, bool KC, int R>
+struct Staged {
+  static constexpr int EPC = 16 / EL::BYTES;       // elements of a chunk
+  static constexpr int BK = 128 / EL::BYTES;       // reduction of a stage
+  static constexpr int CPK = R / EPC;              // MC: chunks of a k row
+  static __device__ __forceinline__ int row(int c) { return KC ? c >> 3 : c / CPK; }  // KC: operand row; MC: k
+  static __device__ __forceinline__ int chunk(int c) {                               // along the other axis
+    if constexpr (KC) {
+      return (c & 7) ^ ((c >> 4) & 7);
+    } else if constexpr (EL::BYTES == 2) {
+      const int q = c % CPK, k = c / CPK;
+      return ((((q >> 1) ^ ((k & 3) << 1)) << 1) | (q & 1));
+    } else {
+      return c % CPK;
+    }
+  }
+
+  // Where this lane's fragments of the 32 rows or columns from `block` on (a multiple of 32) begin. Blocks
+  // that differ by the bits of `flip` in at() share it.
+  static __device__ __forceinline__ int base(int block, int lane) {
+    const int l32 = lane & 31, g2 = lane >> 5;
+    if constexpr (KC) {
+      return (block + l32) * 128;
+    } else if constexpr (EL::BYTES == 2) {
+      const int g = lane >> 4, jj = lane & 15;  // the transposing read works on groups of sixteen lanes
+      return (8 * (g >> 1) + (jj >> 2)) * (R * 2) + 8 * (jj & 3) + (((block / 16 + (g & 1)) ^ ((jj >> 2) << 1)) << 5);
+    } else {
+      return 4 * g2 * (R * 4) + (block + l32) * 4;
+    }
+  }
+  // The fragment of step kk from a base; `nt`: blocks of 32 further on (MC bf16: base's block has zeros in
+  // the bits of nt)
+  static __device__ __forceinline__ i32x4_t frag(const unsigned char* st, int base, int nt, int kk, int lane) {
+    if constexpr (KC) {
+      const int at = base + nt * 32 * 128 + (((2 * kk + (lane >> 5)) ^ ((lane >> 1) & 7)) << 4);
+      return *reinterpret_cast<const i32x4_t*>(st + at);
+    } else if constexpr (EL::BYTES == 2) {
+      const unsigned char* p = st + (base ^ (nt << 6)) + kk * 16 * (R * 2);
+      const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS i16x4_t*)(p));
+      const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS i16x4_t*)(p + 4 * (R * 2)));
+      return __builtin_bit_cast(i32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const unsigned char* p = st + base + nt * 128 + kk * 8 * (R * 4);
+      i32x4_t v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const int*>(p + j * (R * 4));
+      return v;
+    }
+  }
+};
+
+// 16 bytes at element p, of which the first n elements exist (the others read as zero). Any alignment.
+template <class EL>
+__device__ __forceinline__ i32x4_t load_chunk(const typename EL::mem_t* p, int n) {
+  constexpr int EPC = 16 / EL::BYTES;
+  i32x4_t v = {0, 0, 0, 0};
+  if (n >= EPC) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPC; ++i)
+      if (i < n) {
+        if constexpr (EL::BYTES == 4) v[i] = __float_as_int(p[i]);
+        else if constexpr (EL::BYTES == 2) v[i / 2] |= (int)p[i] << (16 * (i & 1));
+        else v[i / 4] |= (int)(uint8_t)p[i] << (8 * (i & 3));
+      }
+  }
+  return v;
+}
+
+// ---- epilogue --------------------------------------------------------------------------
+
+// Eight values of a row: v[0..3] at columns c .. c + 3 and v[4..7] at c + 8 .. c + 11, where c = c0 + 4 (lane / 32);
+// the wave's row block covers columns c0 .. c0 + 15. `vec`: rows are whole 16-byte words of the output.
+template <bool OUT_F32>
+__device__ __forceinline__ void store_run(void* C, size_t row, int N, int c0, int lane, bool ok, bool vec,
+                                          const float (&v)[8]) {
+  const int g2 = lane >> 5;
+  if constexpr (OUT_F32) {
+    float* p = static_cast<float*>(C) + row * N;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + 8 * h + 4 * g2;
+      if (vec) {
+        if (ok && c < N) *reinterpret_cast<float4*>(p + c) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (ok && c + i < N) p[c + i] = v[4 * h + i];
+      }
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(C) + row * N;
+    if (vec) {
+      const uint4 q = pack_row16(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+      const int c = c0 + 8 * g2;
+      if (ok && c < N) *reinterpret_cast<uint4*>(p + c) = q;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + 8 * h + 4 * g2 + i;
+          if (ok && c < N) p[c] = f32_to_bf16_bits(v[4 * h + i]);
+        }
+    }
+  }
+}
+
+// Whether rows of N output values start and end on 16-byte words.
+template <bool OUT_F32>
+__device__ __forceinline__ bool whole_words(const void* C, int N) {
+  return N % (OUT_F32 ? 4 : 8) == 0 && (uintptr_t)C % 16 == 0;
+}
+
+// ---- any sizes, any alignment ----------------------------------------------------------
+//
+// Tiles of 128 x 128 by four waves of 64 x 64. The next stage's chunks are loaded into registers before this
+// one's products and written to LDS after them. TN: rows^T x rows. GATED (INT8): the tile is 64 columns of
+// gate and the same 64 of up, whose 32-column blocks alternate in a wave.
+constexpr int GA_THREADS = 256;
+constexpr int GA_T = 128;
+constexpr int GA_CH = GA_T * 8 / GA_THREADS;  // chunks of an operand that a thread loads per stage
+
+template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED>
+__global__ __launch_bounds__(GA_THREADS) void gg_any_kernel(GgArgs a) {
+  constexpr bool TN = !AKC;
+  using SA = Staged<EL, AKC, GA_T>;
+  using SB = Staged<EL, BKC, GA_T>;
+  using mem_t = typename EL::mem_t;
+  constexpr int BK = SA::BK, EPC = SA::EPC;
+  constexpr int BN = GATED ? 64 : GA_T;
+  __shared__ __attribute__((aligned(16))) unsigned char sm[2 * GA_T * 128];
+  __shared__ int tstart[GG_MAX_E + 1];
+  __shared__ int wsum[GA_THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int ntn = (a.N + BN - 1) / BN;
+  const int mtn = (a.Kd + GA_T - 1) / GA_T;  // TN: row tiles of dW
+  int64_t total;
+  if constexpr (TN) {
+    total = (int64_t)a.E * mtn * ntn;
+  } else {
+    total = group_prefix<GA_THREADS>(a.cu, a.M, a.E, [&](int rows) { return (rows + GA_T - 1) / GA_T * ntn; }, tstart, wsum);
+  }
+  const mem_t* A = static_cast<const mem_t*>(a.A);
+  const bool vec = whole_words<OUT_F32>(a.C, a.N);
+  const int a_base = SA::base(wm * 64, lane), b_base = SB::base(wn * (GATED ? 32 : 64), lane);
+
+  for (int64_t t = xcd_slot(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+    int e, mtile, ntile;
+    if constexpr (TN) {
+      e = (int)(t / ((int64_t)mtn * ntn));
+      const int rem = (int)(t - (int64_t)e * mtn * ntn);
+      mtile = rem / ntn;
+      ntile = rem - mtile * ntn;
+    } else {
+      e = find_expert(tstart, a.E, (int)t);
+    }
+    const int gbeg = group_begin(a.cu, e, a.M);
+    const int rows_e = group_rows(a.cu, e, a.M, gbeg);
+    if constexpr (!TN) {
+      const int mte = (rows_e + GA_T - 1) / GA_T;
+      const int lt = (int)t - tstart[e];
+      ntile = lt / mte;
+      mtile = lt - ntile * mte;
+    }
+    const int m0 = mtile * GA_T, n0 = ntile * BN;
+    const int mvalid = min(GA_T, (TN ? a.Kd : rows_e) - m0);
+    const int red = TN ? rows_e : a.Kd;        // length of the reduction
+    const int nk = (red + BK - 1) / BK;
+    // source rows of the chunks that this thread loads (KC rows of A)
+    int64_t a_row[GA_CH];
+#pragma unroll
+    for (int i = 0; i < GA_CH; ++i) {
+      if constexpr (!TN) {
+        const int r = SA::row(tid + i * GA_THREADS);
+        a_row[i] = -1;
+        if (r < mvalid) {
+          a_row[i] = gbeg + m0 + r;
+          if (a.row_src) {
+            const int src = a.row_src[gbeg + m0 + r];
+            a_row[i] = src < 0 || src / a.a_k >= a.a_rows ? -1 : src / a.a_k;
+          }
+        }
+      }
+    }
+    i32x4_t ra[GA_CH], rb[GA_CH];
+    auto load = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < GA_CH; ++i) {
+        const int c = tid + i * GA_THREADS;
+        const i32x4_t z = {0, 0, 0, 0};
+        ra[i] = rb[i] = z;
+        if constexpr (AKC) {
+          const int k = kt * BK + SA::chunk(c) * EPC;
+          if (a_row[i] >= 0 && k < red) ra[i] = load_chunk<EL>(A + (size_t)a_row[i] * a.Kd + k, red - k);
+        } else {
+          const int k = kt * BK + SA::row(c), col = m0 + SA::chunk(c) * EPC;
+          if (k < red && col < a.Kd) ra[i] = load_chunk<EL>(A + (size_t)(gbeg + k) * a.Kd + col, a.Kd - col);
+        }
+        if constexpr (BKC) {
+          const int r = SB::row(c), k = kt * BK + SB::chunk(c) * EPC;
+          const int n = n0 + (GATED ? r & 63 : r);
+          const mem_t* B = static_cast<const mem_t*>(GATED && r >= 64 ? a.B1 : a.B0);
+          if (n < a.N && k < red) rb[i] = load_chunk<EL>(B + ((size_t)e * a.N + n) * a.Kd + k, red - k);
+        } else {
+          const int k = kt * BK + SB::row(c), col = n0 + SB::chunk(c) * EPC;
+          const size_t brow = TN ? (size_t)(gbeg + k) : (size_t)e * a.Kd + k;
+          if (k < red && col < a.N) rb[i] = load_chunk<EL>(static_cast<const mem_t*>(a.B0) + brow * a.N + col, a.N - col);
+        }
+      }
+    };
+    typename EL::acc_t acc[2][2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[mt][nt][i] = 0;
+    if (nk > 0) load(0);
+    for (int kt = 0; kt < nk; ++kt) {
+      __syncthreads();  // the stage before has been read
+#pragma unroll
+      for (int i = 0; i < GA_CH; ++i) {
+        *reinterpret_cast<i32x4_t*>(sm + (tid + i * GA_THREADS) * 16) = ra[i];
+        *reinterpret_cast<i32x4_t*>(sm + GA_T * 128 + (tid + i * GA_THREADS) * 16) = rb[i];
+      }
+      __syncthreads();
+      if (kt + 1 < nk) load(kt + 1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        i32x4_t fa[2], fb[2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) fa[mt] = SA::frag(sm, a_base, mt, kk, lane);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) fb[nt] = SB::frag(sm + GA_T * 128, b_base, GATED ? 2 * nt : nt, kk, lane);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) EL::mma(acc[mt][nt], fb[nt], fa[mt]);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const int r = wm * 64 + mt * 32 + (lane & 31);
+      const bool ok = r < mvalid;
+      const size_t row = TN ? (size_t)e * a.Kd + m0 + (ok ? r : 0) : (size_t)(gbeg + m0 + (ok ? r : 0));
+      float sa = 1.f;
+      if constexpr (std::is_same<EL, ElI8>::value) {
+        size_t src = row;
+        bool have = ok;
+        if (a.row_src) {
+          const int v = a.row_src[row];
+          have = ok && v >= 0 && v / a.a_k < a.a_rows;
+          src = have ? v / a.a_k : 0;
+        }
+        sa = have ? a.a_sf[src] : 0.f;
+      }
+#pragma unroll
+      for (int nt = 0; nt < (GATED ? 1 : 2); ++nt)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int c0 = n0 + wn * (GATED ? 32 : 64) + nt * 32 + 16 * p;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = c0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+            if constexpr (std::is_same<EL, ElI8>::value) {
+              const size_t sb = (size_t)e * a.N + min(c, a.N - 1);
+              v[i] = sa == 0.f ? 0.f : (float)acc[mt][nt][8 * p + i] * sa * a.b_sf0[sb];
+              if constexpr (GATED)
+                v[i] = sa == 0.f ? 0.f : silu_f32(v[i]) * ((float)acc[mt][1][8 * p + i] * sa * a.b_sf1[sb]);
+            } else {
+              v[i] = acc[mt][nt][8 * p + i];
+              if (TN && OUT_F32 && a.accumulate && ok && c < a.N) v[i] += static_cast<const float*>(a.C)[row * a.N + c];
+            }
+          }
+          store_run<OUT_F32>(a.C, row, a.N, c0, lane, ok, vec, v);
+        }
+    }
+  }
+}
+
+// Tiles of a launch are counted in 31 bits by the callers' checks.
+template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED = false>
+moe_status_t launch_gg_any(const GgArgs& a, hipStream_t s) {
+  gg_any_kernel<EL, AKC, BKC, OUT_F32, GATED><<<4 * device_cu_count(), GA_THREADS, 0, s>>>(a);
+  return launch_status();
+}
+
+}  // namespace moe

@@ -7,6 +7,7 @@
 #include <cstring>
 #include <limits>
 
+#include "grouped_args.h"
 #include "moe_common.h"
 #include "noalloc.h"
 
@@ -78,6 +79,18 @@ moe_status_t launch_combine_bwd(const void* dout, const void* y, const int* pos,
                                 int T, int H, int K, void* dy, float* dw, hipStream_t s);
 moe_status_t launch_route_bwd(const int* idx, const float* w, const float* dw, int T, int E, int K,
                               float* dl, hipStream_t s);
+
+moe_status_t launch_quantize_int8(const void* x, moe_dtype_t xt, int R, int C, int8_t* q, float* sf, hipStream_t s);
+moe_status_t launch_dequantize_int8(const int8_t* q, const float* sf, int R, int C, void* out, moe_dtype_t ot,
+                                    hipStream_t s);
+moe_status_t launch_quantize_int8_weights(const void* w, moe_dtype_t wt, int E, int K, int N, int8_t* q, float* sf,
+                                          hipStream_t s);
+moe_status_t launch_dequantize_int8_weights(const int8_t* q, const float* sf, int E, int K, int N, void* out,
+                                            moe_dtype_t ot, hipStream_t s);
+moe_status_t launch_matmul_int8(const GgArgs& a, moe_dtype_t out, hipStream_t s);
+moe_status_t launch_gate_up_int8(const GgArgs& a, hipStream_t s);
+moe_status_t launch_grouped_matmul(const GgArgs& a, moe_dtype_t dt, bool transposed, moe_dtype_t out, hipStream_t s);
+moe_status_t launch_grouped_wgrad(const GgArgs& a, moe_dtype_t dt, moe_dtype_t out, hipStream_t s);
 
 int device_cu_count() {
   static int cache[64] = {0};
@@ -475,6 +488,239 @@ moe_status_t moe_grouped_ffn_mxfp4(const uint8_t* x_q, const uint8_t* x_sf, cons
                              h_sf, stream);
   if (st != MOE_OK) return st;
   return moe_ffn_down_mxfp4(h_q, h_sf, cu_seqlens, M, E, H, Hp, w_down, sf_down, y_rows, stream);
+}
+
+static bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
+static size_t elem_bytes(moe_dtype_t d) { return d == MOE_F32 ? 4 : 2; }
+static bool f32_or_bf16(moe_dtype_t d) { return d == MOE_F32 || d == MOE_BF16; }
+
+static moe_status_t check_int8_rows(moe_dtype_t dt, int R, int C) {
+  if (R < 0 || C < 1) return MOE_EINVAL;
+  return f32_or_bf16(dt) ? MOE_OK : MOE_EUNSUPPORTED;
+}
+
+moe_status_t moe_quantize_int8(const void* x, moe_dtype_t x_dtype, int32_t R, int32_t C, int8_t* q, float* sf,
+                               hipStream_t stream) {
+  const moe_status_t st = check_int8_rows(x_dtype, R, C);
+  if (st != MOE_OK || R == 0) return st;
+  if (!x || !q || !sf || !aligned_to(x, elem_bytes(x_dtype)) || !aligned_to(sf, 4)) return MOE_EINVAL;
+  return launch_quantize_int8(x, x_dtype, R, C, q, sf, stream);
+}
+
+moe_status_t moe_dequantize_int8(const int8_t* q, const float* sf, int32_t R, int32_t C, void* out,
+                                 moe_dtype_t out_dtype, hipStream_t stream) {
+  const moe_status_t st = check_int8_rows(out_dtype, R, C);
+  if (st != MOE_OK || R == 0) return st;
+  if (!q || !sf || !out || !aligned_to(out, elem_bytes(out_dtype)) || !aligned_to(sf, 4)) return MOE_EINVAL;
+  return launch_dequantize_int8(q, sf, R, C, out, out_dtype, stream);
+}
+
+static moe_status_t check_int8_weights(moe_dtype_t dt, int E, int K, int N) {
+  if (E < 0 || K < 0 || N < 0) return MOE_EINVAL;
+  if (!f32_or_bf16(dt) || (int64_t)K * N >= 1ll << 40) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_int8_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K, int32_t N, int8_t* q,
+                                       float* sf, hipStream_t stream) {
+  const moe_status_t st = check_int8_weights(w_dtype, E, K, N);
+  if (st != MOE_OK || E == 0 || K == 0 || N == 0) return st;
+  if (!w || !q || !sf || !aligned_to(w, elem_bytes(w_dtype)) || !aligned_to(sf, 4)) return MOE_EINVAL;
+  return launch_quantize_int8_weights(w, w_dtype, E, K, N, q, sf, stream);
+}
+
+moe_status_t moe_dequantize_int8_weights(const int8_t* q, const float* sf, int32_t E, int32_t K, int32_t N, void* out,
+                                         moe_dtype_t out_dtype, hipStream_t stream) {
+  const moe_status_t st = check_int8_weights(out_dtype, E, K, N);
+  if (st != MOE_OK || E == 0 || K == 0 || N == 0) return st;
+  if (!q || !sf || !out || !aligned_to(out, elem_bytes(out_dtype)) || !aligned_to(sf, 4)) return MOE_EINVAL;
+  return launch_dequantize_int8_weights(q, sf, E, K, N, out, out_dtype, stream);
+}
+
+// Sizes that the grouped products share: tiles are counted in 31 bits (at least 64 rows and columns each), and
+// offsets into 256 rows, or into 128 reduction steps of columns, are 32-bit.
+static moe_status_t check_grouped(int64_t M, int64_t E, int64_t H, int64_t N) {
+  if (M < 0 || E < 1 || H < 1 || N < 1) return MOE_EINVAL;
+  if (M > 1 << 30 || E > 1024 || H > 1 << 20 || N > 1 << 20) return MOE_EUNSUPPORTED;
+  return (M / 64 + E) * (N / 64 + 1) >= 1ll << 31 ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+// Gathered rows lie at 32-bit offsets.
+static moe_status_t check_gather(const int32_t* row_src, int64_t T, int K, int64_t row_bytes) {
+  if (!row_src) return MOE_OK;
+  if (T < 0 || K < 1) return MOE_EINVAL;
+  return T * row_bytes >= 1ll << 31 ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+static moe_status_t check_int8_product(int M, int E, int H, int N, const int32_t* row_src, int T, int K) {
+  moe_status_t st = check_grouped(M, E, H, N);
+  if (st == MOE_OK) st = check_gather(row_src, T, K, H);
+  if (st != MOE_OK) return st;
+  // 128 * 128 * H, the largest sum, stays below 2^31
+  return H % 16 || H >= 1 << 17 ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+static GgArgs int8_args(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int T, int K, const int32_t* cu,
+                        int M, int E, int H, int N, const int8_t* w0, const float* sf0, const int8_t* w1,
+                        const float* sf1, void* y) {
+  GgArgs a{};
+  a.A = x_q;
+  a.a_sf = x_sf;
+  a.row_src = row_src;
+  a.a_k = K;
+  a.a_rows = T;
+  a.cu = cu;
+  a.M = M;
+  a.E = E;
+  a.Kd = H;
+  a.N = N;
+  a.B0 = w0;
+  a.B1 = w1;
+  a.b_sf0 = sf0;
+  a.b_sf1 = sf1;
+  a.C = y;
+  return a;
+}
+
+moe_status_t moe_matmul_int8(const int8_t* x_q, const float* x_sf, int32_t M, int32_t H, int32_t N, const int8_t* w_q,
+                             const float* w_sf, void* y, moe_dtype_t out, hipStream_t stream) {
+  const moe_status_t st = check_int8_product(M, 1, H, N, nullptr, 0, 0);
+  if (st != MOE_OK) return st;
+  if (!f32_or_bf16(out)) return MOE_EUNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  if (!x_q || !x_sf || !w_q || !w_sf || !y) return MOE_EINVAL;
+  if (!aligned16(x_q) || !aligned16(w_q) || !aligned_to(x_sf, 4) || !aligned_to(w_sf, 4) ||
+      !aligned_to(y, elem_bytes(out)))
+    return MOE_EINVAL;
+  return launch_matmul_int8(int8_args(x_q, x_sf, nullptr, 0, 0, nullptr, M, 1, H, N, w_q, w_sf, nullptr, nullptr, y),
+                            out, stream);
+}
+
+moe_status_t moe_grouped_matmul_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T, int32_t K,
+                                     const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H, int32_t N,
+                                     const int8_t* w_q, const float* w_sf, void* y_rows, moe_dtype_t out,
+                                     hipStream_t stream) {
+  const moe_status_t st = check_int8_product(M, E, H, N, row_src, T, K);
+  if (st != MOE_OK) return st;
+  if (!f32_or_bf16(out)) return MOE_EUNSUPPORTED;
+  if (!cu_seqlens || !aligned_to(cu_seqlens, 4) || !aligned_to(row_src, 4)) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!x_q || !x_sf || !w_q || !w_sf || !y_rows) return MOE_EINVAL;
+  if (!aligned16(x_q) || !aligned16(w_q) || !aligned_to(x_sf, 4) || !aligned_to(w_sf, 4) ||
+      !aligned_to(y_rows, elem_bytes(out)))
+    return MOE_EINVAL;
+  return launch_matmul_int8(int8_args(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, N, w_q, w_sf, nullptr, nullptr,
+                                      y_rows),
+                            out, stream);
+}
+
+moe_status_t moe_ffn_gate_up_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T, int32_t K,
+                                  const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H, int32_t Hp,
+                                  const int8_t* w_gate, const int8_t* w_up, const float* sf_gate, const float* sf_up,
+                                  void* h, hipStream_t stream) {
+  const moe_status_t st = check_int8_product(M, E, H, Hp, row_src, T, K);
+  if (st != MOE_OK) return st;
+  if (!cu_seqlens || !aligned_to(cu_seqlens, 4) || !aligned_to(row_src, 4)) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!x_q || !x_sf || !w_gate || !w_up || !sf_gate || !sf_up || !h) return MOE_EINVAL;
+  if (!aligned16(x_q) || !aligned16(w_gate) || !aligned16(w_up) || !aligned_to(x_sf, 4) || !aligned_to(sf_gate, 4) ||
+      !aligned_to(sf_up, 4) || !aligned_to(h, 2))
+    return MOE_EINVAL;
+  return launch_gate_up_int8(int8_args(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, sf_gate, w_up, sf_up,
+                                       h),
+                             stream);
+}
+
+size_t moe_grouped_ffn_int8_workspace_bytes(int32_t M, int32_t Hp) {
+  if (M < 0 || Hp < 1 || Hp % 16) return 0;
+  return align_up((size_t)M * Hp * 2, 256) + align_up((size_t)M * Hp, 256) + align_up((size_t)M * 4, 256);
+}
+
+moe_status_t moe_grouped_ffn_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T, int32_t K,
+                                  const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H, int32_t Hp,
+                                  const int8_t* w_gate, const int8_t* w_up, const int8_t* w_down, const float* sf_gate,
+                                  const float* sf_up, const float* sf_down, void* y_rows, void* ws, size_t ws_bytes,
+                                  hipStream_t stream) {
+  moe_status_t st = check_int8_product(M, E, H, Hp, row_src, T, K);
+  if (st == MOE_OK) st = check_int8_product(M, E, Hp, H, nullptr, 0, 0);
+  if (st != MOE_OK) return st;
+  if (!cu_seqlens) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!ws || ws_bytes < moe_grouped_ffn_int8_workspace_bytes(M, Hp)) return MOE_EWORKSPACE;
+  // everything that the later calls would refuse, before the first is enqueued
+  if (!w_down || !sf_down || !y_rows || !aligned16(ws) || !aligned16(w_down) || !aligned_to(sf_down, 4) ||
+      !aligned_to(y_rows, 2))
+    return MOE_EINVAL;
+  for (const void* p : {(const void*)x_q, (const void*)w_gate, (const void*)w_up})
+    if (!p || !aligned16(p)) return MOE_EINVAL;
+  for (const void* p : {(const void*)x_sf, (const void*)sf_gate, (const void*)sf_up, (const void*)cu_seqlens})
+    if (!p || !aligned_to(p, 4)) return MOE_EINVAL;
+  if (!aligned_to(row_src, 4)) return MOE_EINVAL;
+  unsigned char* h = static_cast<unsigned char*>(ws);
+  int8_t* h_q = reinterpret_cast<int8_t*>(h + align_up((size_t)M * Hp * 2, 256));
+  float* h_sf = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(h_q) + align_up((size_t)M * Hp, 256));
+  poison(ws, ws_bytes, stream);
+  st = moe_ffn_gate_up_int8(x_q, x_sf, row_src, T, K, cu_seqlens, M, E, H, Hp, w_gate, w_up, sf_gate, sf_up, h, stream);
+  if (st == MOE_OK) st = moe_quantize_int8(h, MOE_BF16, M, Hp, h_q, h_sf, stream);
+  if (st != MOE_OK) return st;
+  return moe_grouped_matmul_int8(h_q, h_sf, nullptr, 0, 0, cu_seqlens, M, E, Hp, H, w_down, sf_down, y_rows, MOE_BF16,
+                                 stream);
+}
+
+moe_status_t moe_grouped_matmul(const void* x, moe_dtype_t act, const int32_t* row_src, int32_t T, int32_t K,
+                                const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H, int32_t N, const void* w,
+                                moe_dtype_t wgt, int32_t transposed, void* y_rows, moe_dtype_t out,
+                                hipStream_t stream) {
+  moe_status_t st = check_grouped(M, E, H, N);
+  if (st != MOE_OK) return st;
+  if (transposed != 0 && transposed != 1) return MOE_EINVAL;
+  if (!f32_or_bf16(act) || wgt != act || !f32_or_bf16(out) || (act == MOE_F32 && out != MOE_F32))
+    return MOE_EUNSUPPORTED;
+  st = check_gather(row_src, T, K, H * (int64_t)elem_bytes(act));
+  if (st != MOE_OK) return st;
+  if (!cu_seqlens || !aligned_to(cu_seqlens, 4) || !aligned_to(row_src, 4)) return MOE_EINVAL;
+  if (M == 0) return MOE_OK;
+  if (!x || !w || !y_rows || !aligned_to(x, elem_bytes(act)) || !aligned_to(w, elem_bytes(act)) ||
+      !aligned_to(y_rows, elem_bytes(out)))
+    return MOE_EINVAL;
+  GgArgs a{};
+  a.A = x;
+  a.row_src = row_src;
+  a.a_k = K;
+  a.a_rows = T;
+  a.cu = cu_seqlens;
+  a.M = M;
+  a.E = E;
+  a.Kd = H;
+  a.N = N;
+  a.B0 = w;
+  a.C = y_rows;
+  return launch_grouped_matmul(a, act, transposed != 0, out, stream);
+}
+
+moe_status_t moe_grouped_matmul_wgrad(const void* x, const void* dy, moe_dtype_t dtype, const int32_t* cu_seqlens,
+                                      int32_t M, int32_t E, int32_t H, int32_t N, void* dw, moe_dtype_t dw_dtype,
+                                      int32_t accumulate, hipStream_t stream) {
+  const moe_status_t st = check_grouped(M, E, H, N);
+  if (st != MOE_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MOE_EINVAL;
+  if (!f32_or_bf16(dtype) || !f32_or_bf16(dw_dtype)) return MOE_EUNSUPPORTED;
+  if (dw_dtype == MOE_BF16 && (dtype != MOE_BF16 || accumulate)) return MOE_EUNSUPPORTED;
+  if ((int64_t)E * (H / 64 + 1) * (N / 64 + 1) >= 1ll << 31) return MOE_EUNSUPPORTED;
+  if (!cu_seqlens || !aligned_to(cu_seqlens, 4) || !dw || !aligned_to(dw, elem_bytes(dw_dtype))) return MOE_EINVAL;
+  if (M > 0 && (!x || !dy)) return MOE_EINVAL;
+  if (!aligned_to(x, elem_bytes(dtype)) || !aligned_to(dy, elem_bytes(dtype))) return MOE_EINVAL;
+  GgArgs a{};
+  a.A = x;
+  a.cu = cu_seqlens;
+  a.M = M;
+  a.E = E;
+  a.Kd = H;
+  a.N = N;
+  a.B0 = dy;
+  a.C = dw;
+  a.accumulate = accumulate;
+  return launch_grouped_wgrad(a, dtype, dw_dtype, stream);
 }
 
 moe_status_t moe_ffn_gate_up(const void* x_perm, const float* x_perm_sf, moe_dtype_t act,

@@ -229,6 +229,26 @@ def decode_mxfp4_rows(packed: np.ndarray, scales: np.ndarray) -> np.ndarray:
 # ----------------------------------------------------------------------------- routing
 
 
+def quantize_int8(x: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """Rows [R, C] -> INT8 codes and fp32 scales [R]: s = max(fl32(amax / 127), 2^-120), 1 for a
+    zero row; q the nearest integer to x / s, ties to even. A row with a NaN or an infinity: scale NaN,
+    codes 0. float64 decides a code exactly: x - (n + 1/2) s is a multiple of 2^-149 and of s 2^-25, so a
+    quotient that is no tie lies at least 2^-29 from one, far above float64's spacing at 127 (2^-46)."""
+    x = np.asarray(x, dtype=np.float64)
+    amax = np.abs(x).max(axis=1)
+    bad = ~np.isfinite(amax)
+    with np.errstate(invalid="ignore"):
+        s = np.maximum((np.where(bad, 0.0, amax) / 127.0).astype(np.float32), np.float32(2.0 ** -120))
+    s = np.where(amax == 0, np.float32(1.0), s).astype(np.float32)
+    q = np.rint(np.where(bad[:, None], 0.0, x) / s.astype(np.float64)[:, None])
+    return q.astype(np.int8), np.where(bad, np.float32(np.nan), s).astype(np.float32)
+
+
+def decode_int8(q: np.ndarray, s: np.ndarray) -> np.ndarray:
+    """Codes [R, C] and scales [R] -> float64 values (the exact products)."""
+    return q.astype(np.float64) * s.astype(np.float64)[:, None]
+
+
 def masked_logits(logits: np.ndarray, lowest: float) -> np.ndarray:
     """Logits as float64 with masked experts (NaN, -inf, the storage type's lowest value) as
     -inf and +inf as the largest fp32 value."""
