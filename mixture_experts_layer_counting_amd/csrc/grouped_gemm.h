@@ -108,7 +108,7 @@ struct ElF32 {
 // Chunk c lies at byte 16 c and holds:
 //   KC  row c / 8, k chunk (c % 8) ^ (row / 2 % 8): sixteen lanes that read one chunk of sixteen rows
 //       hit all banks once
-//   MC  bf16: k row c / (R / 8), 32-byte segments swizzled by 2 (k % 4), for the transposing reads;
+//   MC  bf16: k row c / (R / 8), 32-byte segments swizzled by k, for the transposing reads;
 //       fp32: k row c / (R / 4), in order
 template <class EL, bool KC, int R>
 struct Staged {
@@ -120,12 +120,16 @@ struct Staged {
     if constexpr (KC) {
       return (c & 7) ^ ((c >> 4) & 7);
     } else if constexpr (EL::BYTES == 2) {
-      const int q = c % CPK, k = c / CPK;
-      return ((((q >> 1) ^ ((k & 3) << 1)) << 1) | (q & 1));
+      const int q = c % CPK;
+      return ((((q >> 1) ^ swizzle(c / CPK)) << 1) | (q & 1));
     } else {
       return c % CPK;
     }
   }
+
+  // MC bf16: a transposing read takes 64 bytes of four k rows, which have to fall on different banks; rows of
+  // 64 columns are half of them long
+  static __device__ __forceinline__ int swizzle(int k) { return R >= 128 ? (k & 3) << 1 : k & 2; }
 
   // Where this lane's fragments of the 32 rows or columns from `block` on (a multiple of 32) begin. Blocks
   // that differ by the bits of `flip` in at() share it.
@@ -135,7 +139,7 @@ struct Staged {
       return (block + l32) * 128;
     } else if constexpr (EL::BYTES == 2) {
       const int g = lane >> 4, jj = lane & 15;  // the transposing read works on groups of sixteen lanes
-      return (8 * (g >> 1) + (jj >> 2)) * (R * 2) + 8 * (jj & 3) + (((block / 16 + (g & 1)) ^ ((jj >> 2) << 1)) << 5);
+      return (8 * (g >> 1) + (jj >> 2)) * (R * 2) + 8 * (jj & 3) + (((block / 16 + (g & 1)) ^ swizzle(jj >> 2)) << 5);
     } else {
       return 4 * g2 * (R * 4) + (block + l32) * 4;
     }

@@ -1,21 +1,43 @@
 // Products of ragged expert groups in bf16 and fp32, and the gradient of their weights ("Distributed
 // expert parallelism", "Grouped expert computation": one launch for every expert's variable-size group;
 // MoonEP "Integration": stacked weights, cu_seqlens selecting each expert's rows).
-#include "grouped_gemm.h"
+#include "grouped_tiles.h"
 
 namespace moe {
 
+namespace {
+
+template <class EL>
+using Large = GtCfg<EL, 4, 2, 2, 4>;
+template <class EL>
+using Small = GtCfg<EL, 2, 2, 2, 2>;
+template <class EL>
+using Narrow = GtCfg<EL, 4, 1, 1, 2>;
+
+template <class EL, bool AKC, bool BKC, bool OUT_F32>
+moe_status_t launch(const GgArgs& a, hipStream_t s) {
+  constexpr int ES = EL::BYTES;
+  // whole 16-byte words along every axis that a load runs along
+  const bool words = (size_t)a.Kd * ES % 16 == 0 && (BKC || (size_t)a.N * ES % 16 == 0) && (uintptr_t)a.A % 16 == 0 &&
+                     (uintptr_t)a.B0 % 16 == 0;
+  if (!words) return launch_gg_any<EL, AKC, BKC, OUT_F32>(a, s);
+  if (a.N <= 64) return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, Narrow<EL>>(a, s);
+  if (few_large_tiles(a, !AKC, a.N)) return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, Small<EL>>(a, s);
+  return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, Large<EL>>(a, s);
+}
+
+}  // namespace
+
 moe_status_t launch_grouped_matmul(const GgArgs& a, moe_dtype_t dt, bool transposed, moe_dtype_t out, hipStream_t s) {
-  if (dt == MOE_F32) return transposed ? launch_gg_any<ElF32, true, true, true>(a, s) : launch_gg_any<ElF32, true, false, true>(a, s);
-  if (out == MOE_F32)
-    return transposed ? launch_gg_any<ElBf16, true, true, true>(a, s) : launch_gg_any<ElBf16, true, false, true>(a, s);
-  return transposed ? launch_gg_any<ElBf16, true, true, false>(a, s) : launch_gg_any<ElBf16, true, false, false>(a, s);
+  if (dt == MOE_F32) return transposed ? launch<ElF32, true, true, true>(a, s) : launch<ElF32, true, false, true>(a, s);
+  if (out == MOE_F32) return transposed ? launch<ElBf16, true, true, true>(a, s) : launch<ElBf16, true, false, true>(a, s);
+  return transposed ? launch<ElBf16, true, true, false>(a, s) : launch<ElBf16, true, false, false>(a, s);
 }
 
 moe_status_t launch_grouped_wgrad(const GgArgs& a, moe_dtype_t dt, moe_dtype_t out, hipStream_t s) {
-  if (dt == MOE_F32) return launch_gg_any<ElF32, false, false, true>(a, s);
-  if (out == MOE_F32) return launch_gg_any<ElBf16, false, false, true>(a, s);
-  return launch_gg_any<ElBf16, false, false, false>(a, s);
+  if (dt == MOE_F32) return launch<ElF32, false, false, true>(a, s);
+  if (out == MOE_F32) return launch<ElBf16, false, false, true>(a, s);
+  return launch<ElBf16, false, false, false>(a, s);
 }
 
 }  // namespace moe
