@@ -1,18 +1,12 @@
 // Products of ragged expert groups in bf16 and fp32, and the gradient of their weights ("Distributed
 // expert parallelism", "Grouped expert computation": one launch for every expert's variable-size group;
 // MoonEP "Integration": stacked weights, cu_seqlens selecting each expert's rows).
+#include "grouped_stream.h"
 #include "grouped_tiles.h"
 
 namespace moe {
 
 namespace {
-
-template <class EL>
-using Large = GtCfg<EL, 4, 2, 2, 4>;
-template <class EL>
-using Small = GtCfg<EL, 2, 2, 2, 2>;
-template <class EL>
-using Narrow = GtCfg<EL, 4, 1, 1, 2>;
 
 template <class EL, bool AKC, bool BKC, bool OUT_F32>
 moe_status_t launch(const GgArgs& a, hipStream_t s) {
@@ -21,9 +15,15 @@ moe_status_t launch(const GgArgs& a, hipStream_t s) {
   const bool words = (size_t)a.Kd * ES % 16 == 0 && (BKC || (size_t)a.N * ES % 16 == 0) && (uintptr_t)a.A % 16 == 0 &&
                      (uintptr_t)a.B0 % 16 == 0;
   if (!words) return launch_gg_any<EL, AKC, BKC, OUT_F32>(a, s);
-  if (a.N <= 64) return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, Narrow<EL>>(a, s);
-  if (few_large_tiles(a, !AKC, a.N)) return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, Small<EL>>(a, s);
-  return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, Large<EL>>(a, s);
+  switch (gg_form(a, !AKC, ES == 4, a.N)) {
+    case GG_STREAM:  // (not where rows are gathered from no token at all)
+      if constexpr (AKC)
+        if (!a.row_src || a.a_rows > 0) return launch_gg_stream<EL, BKC, OUT_F32, false>(a, s);
+      [[fallthrough]];
+    case GG_THIN: return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, GtThin<EL>>(a, s);
+    case GG_SMALL: return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, GtSmall<EL>>(a, s);
+    default: return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, GtLarge<EL>>(a, s);
+  }
 }
 
 }  // namespace

@@ -12,22 +12,26 @@
 
 namespace moe {
 
+constexpr int GT_PANEL = 8;
 constexpr int GT_OUT = (int)0x80000000u;  // an offset past every range: loads zeros
 
-template <class EL, int WM_, int WN_, int MT_, int NT_>
+template <class EL, int WM_, int WN_, int MT_, int NT_, int NS_ = 2>
 struct GtCfg {
   static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+  static constexpr int NS = NS_;  // stages in LDS
   static constexpr int W = WM * WN, THREADS = 64 * W;
   static constexpr int BM = WM * MT * 32, BN = WN * NT * 32;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int LDA = BM / (8 * W), LDB = BN / (8 * W);  // wave loads per stage
   static constexpr bool SCALED = std::is_same<EL, ElI8>::value;
-  static constexpr int SC_BYTES = SCALED ? (BM + BN) * 4 : 0;   // scales of a tile's rows and columns, twice
-  static constexpr int SC_LD = SCALED ? (BM + BN) / 64 / W : 0;
-  static constexpr int SCHED = 2 * STAGE + 2 * SC_BYTES;
+  // scales of a tile's rows and columns, twice (gated: both matrices' columns, in runs of 64 at least)
+  static constexpr int SC_WAVES = SCALED ? (BM + (BN > 128 ? BN : 128)) / 64 : 0;
+  static constexpr int SC_BYTES = SC_WAVES * 256;
+  static constexpr int SC_LD = (SC_WAVES + W - 1) / W;
+  static constexpr int SCHED = NS * STAGE + 2 * SC_BYTES;
   static constexpr int LDS = SCHED + (GG_MAX_E + 1 + W) * 4;
   static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && (4 * W) % 8 == 0, "whole wave loads, one swizzle per lane");
-  static_assert(!SCALED || ((BM + BN) / 64 % W == 0 && BM % (64 * 1) == 0), "whole wave loads of scales");
+  static_assert(BM % 64 == 0 && LDA + LDB <= 31, "whole wave loads of scales; waits count to 63");
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
@@ -36,6 +40,10 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   constexpr bool TN = !AKC;
   constexpr int W = CF::W, BM = CF::BM, MT = CF::MT, NT = CF::NT;
   constexpr int BN = GATED ? CF::BN / 2 : CF::BN;  // columns per matrix
+  constexpr int SCN = BN < 64 ? 64 : BN;           // and their places among the scales
+  constexpr int NS = CF::NS;
+  // fp32 gradients leave with a column per lane, 128 neighbouring bytes of two rows a store
+  constexpr bool COL_LANES = TN && OUT_F32;
   using SA = Staged<EL, AKC, BM>;
   using SB = Staged<EL, BKC, CF::BN>;
   constexpr int BK = SA::BK, ES = EL::BYTES;
@@ -99,8 +107,11 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
     } else {
       const int lt = t - tstart[d.e];
       const int mte = (rows_e + BM - 1) / BM;
-      ntile = lt / mte;
-      mtile = lt - ntile * mte;
+      // eight row tiles under one column tile, then the next column tile: the blocks of an XCD share rows and columns
+      const int panel = lt / (GT_PANEL * ntn), in_panel = lt - panel * GT_PANEL * ntn;
+      const int deep = min(GT_PANEL, mte - panel * GT_PANEL);
+      ntile = in_panel / deep;
+      mtile = panel * GT_PANEL + in_panel - ntile * deep;
       const int chunk = even_chunk(rows_e, mte);
       d.row0 = uniform(d.gbeg + mtile * chunk);
       d.rows_valid = uniform(min(chunk, rows_e - mtile * chunk));
@@ -157,8 +168,8 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       // scales: rows then columns; a column's offset goes from the tile's first one
 #pragma unroll
       for (int i = 0; i < CF::SC_LD; ++i) {
-        const int c = (wave + W * i) * 64 - BM + lane;
-        if ((wave + W * i) * 64 >= BM) d.sc_off[i] = d.n0 + (GATED ? c % BN : c) < N ? (GATED ? c % BN : c) * 4 : GT_OUT;
+        const int c = ((wave + W * i) * 64 - BM + lane) % SCN;
+        if ((wave + W * i) * 64 >= BM) d.sc_off[i] = c < BN && d.n0 + c < N ? c * 4 : GT_OUT;
       }
     }
     return d;
@@ -195,12 +206,13 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
 #pragma unroll
     for (int i = 0; i < CF::SC_LD; ++i) {
       const int at = (wave + W * i) * 64;
-      const uint32_t to = lds0 + 2 * CF::STAGE + par * CF::SC_BYTES + at * 4;
+      const uint32_t to = lds0 + NS * CF::STAGE + par * CF::SC_BYTES + at * 4;
+      if (at >= BM + (GATED ? 2 : 1) * SCN) break;
       if (at < BM) {
         if (a.row_src) lds_dma4(make_rsrc(a.a_sf, (uint32_t)a.a_rows * 4u), to, d.sc_off[i], 0);
         else lds_dma4(make_rsrc(a.a_sf + d.row0, (uint32_t)d.rows_valid * 4u), to, d.sc_off[i], 0);
       } else {
-        const float* sf = GATED && at - BM >= BN ? a.b_sf1 : a.b_sf0;
+        const float* sf = GATED && at - BM >= SCN ? a.b_sf1 : a.b_sf0;
         lds_dma4(make_rsrc(sf + (size_t)d.e * N + d.n0, (uint32_t)(N - d.n0) * 4u), to, d.sc_off[i], 0);
       }
     }
@@ -214,9 +226,11 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   const int b_base = SB::base(wn * (GATED ? NT / 2 : NT) * 32, lane);
   const bool vec = whole_words<OUT_F32>(a.C, N);
 
-  int buf = 0, par = 0;
+  auto after = [](int b) __attribute__((always_inline)) { return b + 1 == NS ? 0 : b + 1; };
+  auto before = [](int b) __attribute__((always_inline)) { return b == 0 ? NS - 1 : b - 1; };
+  int buf = 0, ahead = 1, par = 0;
   Tile cur, nxt;
-  if (slot < total) {
+  if (NS == 2 && slot < total) {
     cur = decode(slot);
     if (CF::SCALED) issue_scales(cur, par);
     if (cur.nk > 0) load_all(cur, 0, buf);
@@ -262,7 +276,8 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
         gg_for<PRODUCTS>([&](auto m_) __attribute__((always_inline)) {
           constexpr int m = decltype(m_)::value;
           constexpr int mt = m % MR, nt = m / MR;
-          EL::mma(acc[mt][nt], f.b[nt], f.a[mt]);
+          if constexpr (COL_LANES) EL::mma(acc[mt][nt], f.a[mt], f.b[nt]);
+          else EL::mma(acc[mt][nt], f.b[nt], f.a[mt]);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (kk_next >= 0) {
             constexpr int per = (READS + PRODUCTS - 1) / PRODUCTS;
@@ -274,7 +289,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
             constexpr int per = (PIECES + PRODUCTS - 1) / PRODUCTS;
             if (load)
               gg_for<per>([&](auto i_) __attribute__((always_inline)) {
-                piece(d, kt, buf ^ 1, std::integral_constant<int, per * m + decltype(i_)::value>{});
+                piece(d, kt, ahead, std::integral_constant<int, per * m + decltype(i_)::value>{});
               });
           }
           __builtin_amdgcn_sched_barrier(0);
@@ -286,51 +301,91 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
         step(f1, f0, st, integral_constant<int, 2>{}, std::false_type{}, cur, 0, false);
         step(f0, f1, st, integral_constant<int, 3>{}, std::false_type{}, cur, 0, false);
       };
-      // Stage kt: it has landed for every wave, and every wave has read all it needs of the other buffer, into which stage
-      // `kl` of tile d goes.
-      auto stage = [&](const Tile& d, int kl, bool load) __attribute__((always_inline)) {
+      // A stage: it has landed for every wave (at most `younger` loads are outstanding), and every wave has read all
+      // it needs of the buffer before it, into which stage `kl` of tile d goes.
+      auto stage = [&](const Tile& d, int kl, bool load, int younger) __attribute__((always_inline)) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        wait_barrier<0>();
+        wait_vm_dyn<(NS - 2) * PIECES>(younger);
+        asm volatile("s_barrier" ::: "memory");
+        ahead = before(buf);
         if constexpr (MTV > 0) {
           const unsigned char* st = smem + buf * CF::STAGE;
           step(f1, f0, st, integral_constant<int, 0>{}, std::true_type{}, d, kl, load);
           rest(st);
         } else if (load) {
-          load_all(d, kl, buf ^ 1);
+          load_all(d, kl, ahead);
         }
-        buf ^= 1;
+        buf = after(buf);
       };
       if constexpr (MTV > 0) {
         const unsigned char* st = smem + buf * CF::STAGE;
         gg_for<READS>([&](auto i_) __attribute__((always_inline)) { read_one(f0, st, integral_constant<int, 0>{}, i_); });
         rest(st);
       }
-      buf ^= 1;
+      buf = after(buf);
       const int nk = cur.nk;
-      for (int kt = 1; kt + 1 < nk; ++kt) stage(cur, kt + 1, true);
-      if (nk > 1) stage(nxt, 0, nxt_load);
+      if constexpr (NS == 2) {
+        for (int kt = 1; kt + 1 < nk; ++kt) stage(cur, kt + 1, true, 0);
+        if (nk > 1) stage(nxt, 0, nxt_load, 0);
+      } else {
+        for (int kt = 1; kt < nk; ++kt) stage(cur, kt + NS - 1, kt + NS - 1 < nk, min(NS - 2, nk - 1 - kt) * PIECES);
+      }
       if constexpr (MTV > 0) step(f1, f0, smem, integral_constant<int, -1>{}, std::false_type{}, cur, 0, false);
     };
-    // every wave waited for its loads of this tile's first stage; the reads of the last tile's are done
+    // (NS = 2: every wave waited for its loads of this tile's first stage); the reads of the last tile's are done
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (cur.nk > 1) load_all(cur, 1, buf ^ 1);
-    if (more) {
-      nxt = decode(t + G);
-      nxt_load = nxt.nk > 0;
-      if (CF::SCALED) issue_scales(nxt, par ^ 1);
-      if (nxt_load && cur.nk < 2) load_all(nxt, 0, cur.nk ? buf ^ 1 : buf);  // a longer tile: under its last stage
+    if constexpr (NS == 2) {
+      if (cur.nk > 1) load_all(cur, 1, buf ^ 1);
+      if (more) {
+        nxt = decode(t + G);
+        nxt_load = nxt.nk > 0;
+        if (CF::SCALED) issue_scales(nxt, par ^ 1);
+        if (nxt_load && cur.nk < 2) load_all(nxt, 0, cur.nk ? buf ^ 1 : buf);  // a longer tile: under its last stage
+      }
+    } else {
+      // all stages that fit, and a wait for the first (the last tile's stores and the scales are older)
+      cur = decode(t);
+      if (CF::SCALED) issue_scales(cur, par);
+      buf = 0;
+      const int first = min(NS, cur.nk);
+      for (int st = 0; st < first; ++st) load_all(cur, st, st);
+      wait_vm_dyn<(NS - 1) * PIECES>((first - 1) * PIECES);
+      asm volatile("s_barrier" ::: "memory");
     }
     if constexpr (TN) {
       if (cur.nk > 0) k_loop(std::integral_constant<int, MT>{});
     } else {
       static_assert(MT <= 2, "the cases below");
-      if (MT == 2 && cur.nmt == 2) k_loop(std::integral_constant<int, MT>{});
-      else if (cur.nmt == 1) k_loop(std::integral_constant<int, 1>{});
+      if (cur.nmt == MT) k_loop(std::integral_constant<int, MT>{});
+      else if (MT > 1 && cur.nmt == 1) k_loop(std::integral_constant<int, 1>{});
       else k_loop(std::integral_constant<int, 0>{});
     }
     wait_vm<0>();
 
-    const float* sc = reinterpret_cast<const float*>(smem + 2 * CF::STAGE + par * CF::SC_BYTES);
+    if constexpr (COL_LANES) {
+      // lane l holds column l % 32 and, in acc[4 j + c], row 8 j + 4 (l / 32) + c
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int col = cur.n0 + wn * NT * 32 + nt * 32 + (lane & 31);
+          const int r0 = mt * CF::WM * 32 + wm * 32 + 4 * (lane >> 5);
+          float* p = static_cast<float*>(a.C) + ((size_t)cur.e * Kd + cur.row0 + r0) * N + col;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int dr = 8 * (i >> 2) + (i & 3);
+            if (col < N && r0 + dr < cur.rows_valid) {
+              float v = acc[mt][nt][i];
+              if (a.accumulate) v += p[(size_t)dr * N];
+              p[(size_t)dr * N] = v;
+            }
+          }
+        }
+      if (NS == 2) cur = nxt;
+      par ^= 1;
+      continue;
+    }
+    const float* sc = reinterpret_cast<const float*>(smem + NS * CF::STAGE + par * CF::SC_BYTES);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (!TN && mt >= cur.nmt) break;
@@ -352,7 +407,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
             const int cl = cw + 16 * p + 8 * h + 4 * (lane >> 5);
             if constexpr (CF::SCALED) {
               s0 = *reinterpret_cast<const f32x4_t*>(sc + BM + cl);
-              if constexpr (GATED) s1 = *reinterpret_cast<const f32x4_t*>(sc + BM + BN + cl);
+              if constexpr (GATED) s1 = *reinterpret_cast<const f32x4_t*>(sc + BM + SCN + cl);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -374,17 +429,55 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
         }
       }
     }
-    cur = nxt;
+    if (NS == 2) cur = nxt;
     par ^= 1;
   }
 }
 
-// Whether tiles of 256 x 256 leave CUs without one: as many groups as can have rows, evenly filled.
-inline bool few_large_tiles(const GgArgs& a, bool tn, int columns) {
-  const int64_t across = (columns + 255) / 256;
-  const int64_t groups = a.M < a.E ? a.M : a.E;
-  const int64_t tiles = tn ? (int64_t)a.E * ((a.Kd + 255) / 256) * across : (groups + (a.M - groups) / 256) * across;
-  return tiles < device_cu_count();
+// The forms of the kernel: 256 x 256 by eight waves; 128 x 128 by four, two blocks a CU; 128 x 64 by four with four
+// stages in LDS, for products whose tiles are so few that the loads' latency counts.
+// (Large with two waves down and four across, which halves the rows a wave may skip, took 1.5-2.5 % longer on every
+// shape: INT8, 65536 rows over 52 experts, 7168 x 2048 883 us beside 863.)
+template <class EL>
+using GtLarge = GtCfg<EL, 4, 2, 2, 4>;
+template <class EL>
+using GtSmall = GtCfg<EL, 2, 2, 2, 2>;
+template <class EL>
+using GtThin = GtCfg<EL, 4, 1, 1, 2, 4>;
+
+enum GgForm { GG_STREAM, GG_THIN, GG_SMALL, GG_LARGE };
+
+// Which kernel takes a product whose rows are whole 16-byte words, from the number of 128 x 64 tiles (`thin`; of both matrices
+// where gated) and the rows per group. Measured on 256 CUs, us, stream / thin / small / large, rows per group in brackets:
+//   INT8, dense 7168 x 2048 (32 thin tiles): [1] 7.5 / 23 / 35 / 50  [16] 10 / 23 / 36 / 50  [64] 16 / 23 / 38 / 54
+//                                           [128] 30 / 25 / 43 / 54  [2048, 512 tiles] - / 50 / 58 / 99  [4096] - / 130 / 62 / 103
+//   INT8, 8 experts 7168 x 2048 (256): [1] 24 / 24 / 49 / 57  [16] 31 / 25 / 50 / 57  [128] 200 / 27 / 62 / 67
+//   INT8 gate/up, the same (512): [1] 40 / 49 / 63 / 67  [8] 47 / 49 / 63 / 67  [16] 57 / 49 / 64 / 67
+//   INT8, 8 experts 2048 x 7168 (896): [1] 25 / 34 / 22 / 24  [16] 35 / 33 / 23 / 25
+//   bf16 [K][N], 8 experts 7168 x 2048 (256): [1] 37 / 44 / 93 / 103  [16] 39 / 44 / 94 / 102  [128] 158 / 48 / 110 / 115
+//   bf16 [K][N], 16 experts 1024 x 512 (128): [1] 6.8 / 9.6 / 17 / 18  [16] 7.3 / 9.8 / 18 / 19  [64] 11 / 10 / 20 / 21
+//   bf16 [K][N], 64 experts 2048 x 1024 (1024): [32] 66 / 56 / 44 / 47  [128] 220 / 80 / 58 / 60  [384] - / - / 148 / 122
+//   fp32 [K][N], 8 experts 7168 x 2048 (256): [16] 89 / 260 / 425 / 458  [32] 141 / 260 / 429 / 463  [64] 251 / 262 / 433 / 467
+//   fp32 [K][N], 64 experts 2048 x 1024 (1024): [1] 98 / 303 / 128 / 139  [16] 102 / 303 / 129 / 140
+//   dW, 64 experts 2048 x 24 (384 rows; 1024): - / 22 / 22 / 28, 24 x 2048 (2048): - / 38 / 23 / 34
+//   dW, one expert 1024 x 1024 (8192 rows; 128): - / 50 / 87 / 150, 7168 x 2048 (1792): - / 352 / 243 / 204
+inline GgForm gg_form(const GgArgs& a, bool tn, bool f32, int columns) {
+  const int64_t cus = device_cu_count();
+  const int64_t slots = tn || a.E < a.M ? a.E : a.M;  // at most so many groups have rows
+  auto tiles = [&](int bm, int bn) -> int64_t {
+    const int64_t down = tn ? slots * ((a.Kd + bm - 1) / bm) : slots + (a.M - slots) / bm;
+    return down * ((columns + bn - 1) / bn);
+  };
+  const int64_t thin = tiles(128, 64);
+  if (!tn) {
+    if (a.M <= 16 * slots && thin <= (f32 ? 4 : 1) * cus) return GG_STREAM;
+    if (a.M <= 8 * slots && thin <= 2 * cus) return GG_STREAM;
+    if (a.M <= 32 * slots && (f32 ? 1 : 4) * thin <= cus) return GG_STREAM;
+    if (a.M <= 64 * slots && 8 * thin <= cus) return GG_STREAM;
+  }
+  if (thin <= 2 * cus || (!tn && columns <= 64)) return GG_THIN;
+  const bool narrow = columns <= 64 || (tn && a.Kd <= 64);
+  return !narrow && (tn || a.M > 128 * slots) && 4 * tiles(256, 256) >= 3 * cus ? GG_LARGE : GG_SMALL;
 }
 
 template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED, class CF>
