@@ -74,7 +74,6 @@ __device__ __forceinline__ void gg_for(F&& f) {
 // ---- element types ---------------------------------------------------------------------
 
 struct ElBf16 {
-  using mem_t = uint16_t;
   using acc_t = f32x16_t;
   static constexpr int BYTES = 2;
   static __device__ __forceinline__ void mma(acc_t& acc, i32x4_t b, i32x4_t a) {
@@ -84,7 +83,6 @@ struct ElBf16 {
 };
 
 struct ElI8 {
-  using mem_t = int8_t;
   using acc_t = i32x16_t;
   static constexpr int BYTES = 1;
   static __device__ __forceinline__ void mma(acc_t& acc, i32x4_t b, i32x4_t a) {
@@ -93,7 +91,6 @@ struct ElI8 {
 };
 
 struct ElF32 {
-  using mem_t = float;
   using acc_t = f32x16_t;
   static constexpr int BYTES = 4;
   static __device__ __forceinline__ void mma(acc_t& acc, i32x4_t b, i32x4_t a) {
@@ -165,21 +162,25 @@ struct Staged {
   }
 };
 
-// 16 bytes at element p, of which the first n elements exist (the others read as zero). Any alignment.
-template <class EL>
-__device__ __forceinline__ i32x4_t load_chunk(const typename EL::mem_t* p, int n) {
-  constexpr int EPC = 16 / EL::BYTES;
+// Eight bf16 at p, at any alignment. What lies past `end`, the operand's last element, reads as zeros.
+__device__ __forceinline__ i32x4_t load_chunk(const uint16_t* p, const uint16_t* end) {
   i32x4_t v = {0, 0, 0, 0};
-  if (n >= EPC) {
+  if (p + 8 <= end) {
     __builtin_memcpy(&v, p, 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < EPC; ++i)
-      if (i < n) {
-        if constexpr (EL::BYTES == 4) v[i] = __float_as_int(p[i]);
-        else if constexpr (EL::BYTES == 2) v[i / 2] |= (int)p[i] << (16 * (i & 1));
-        else v[i / 4] |= (int)(uint8_t)p[i] << (8 * (i & 3));
-      }
+    for (int i = 0; i < 8; ++i)
+      if (p + i < end) v[i / 2] |= (int)p[i] << (16 * (i & 1));
+  }
+  return v;
+}
+
+// The first n elements of a chunk; the others zero.
+__device__ __forceinline__ i32x4_t first_of_chunk(i32x4_t v, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i >= n) v[i] = 0;
+    else if (2 * i + 1 >= n) v[i] &= 0xffff;
   }
   return v;
 }
@@ -229,169 +230,169 @@ __device__ __forceinline__ bool whole_words(const void* C, int N) {
   return N % (OUT_F32 ? 4 : 8) == 0 && (uintptr_t)C % 16 == 0;
 }
 
-// ---- any sizes, any alignment ----------------------------------------------------------
+// ---- bf16 rows that are not whole 16-byte words --------------------------------------------
 //
-// Tiles of 128 x 128 by four waves of 64 x 64. The next stage's chunks are loaded into registers before this
-// one's products and written to LDS after them. TN: rows^T x rows. GATED (INT8): the tile is 64 columns of
-// gate and the same 64 of up, whose 32-column blocks alternate in a wave.
+// Tiles of T x T by four waves; a thread loads its chunks of a stage into
+// registers PD stages ahead and writes them to one of two LDS buffers. A chunk that reaches past its row reads the next row's elements,
+// which count for columns that are not stored or are cut off in the last stage of the reduction. TN: rows^T x rows.
 constexpr int GA_THREADS = 256;
-constexpr int GA_T = 128;
-constexpr int GA_CH = GA_T * 8 / GA_THREADS;  // chunks of an operand that a thread loads per stage
 
-template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED>
-__global__ __launch_bounds__(GA_THREADS) void gg_any_kernel(GgArgs a) {
+template <bool AKC, bool BKC, bool OUT_F32, int T, int PD>
+__global__ __launch_bounds__(GA_THREADS, 2) void gg_any_kernel(GgArgs a) {
   constexpr bool TN = !AKC;
-  using SA = Staged<EL, AKC, GA_T>;
-  using SB = Staged<EL, BKC, GA_T>;
-  using mem_t = typename EL::mem_t;
+  using EL = ElBf16;
+  using SA = Staged<EL, AKC, T>;
+  using SB = Staged<EL, BKC, T>;
+  using mem_t = uint16_t;
   constexpr int BK = SA::BK, EPC = SA::EPC;
-  constexpr int BN = GATED ? 64 : GA_T;
-  __shared__ __attribute__((aligned(16))) unsigned char sm[2 * GA_T * 128];
-  __shared__ int tstart[GG_MAX_E + 1];
-  __shared__ int wsum[GA_THREADS / 64];
+  constexpr int CH = T * 8 / GA_THREADS;  // chunks of an operand that a thread loads per stage
+  constexpr int W = T / 64;               // blocks of 32 x 32 of a wave along each axis
+  constexpr int STAGE = 2 * T * 128;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  int* tstart = reinterpret_cast<int*>(smem + 2 * STAGE);
+  int* wsum = tstart + GG_MAX_E + 1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const int ntn = (a.N + BN - 1) / BN;
-  const int mtn = (a.Kd + GA_T - 1) / GA_T;  // TN: row tiles of dW
-  int64_t total;
-  if constexpr (TN) {
-    total = (int64_t)a.E * mtn * ntn;
-  } else {
-    total = group_prefix<GA_THREADS>(a.cu, a.M, a.E, [&](int rows) { return (rows + GA_T - 1) / GA_T * ntn; }, tstart, wsum);
-  }
+  const int ntn = (a.N + T - 1) / T;
+  const int mtn = (a.Kd + T - 1) / T;  // TN: row tiles of dW
+  int total;
+  if constexpr (TN) total = a.E * mtn * ntn;
+  else total = group_prefix<GA_THREADS>(a.cu, a.M, a.E, [&](int rows) { return (rows + T - 1) / T * ntn; }, tstart, wsum);
   const mem_t* A = static_cast<const mem_t*>(a.A);
+  const mem_t* B = static_cast<const mem_t*>(a.B0);
+  const mem_t* a_end = A + (size_t)(a.row_src ? a.a_rows : a.M) * a.Kd;
+  const mem_t* b_end = B + (TN ? (size_t)a.M * a.N : (size_t)a.E * a.Kd * a.N);
   const bool vec = whole_words<OUT_F32>(a.C, a.N);
-  const int a_base = SA::base(wm * 64, lane), b_base = SB::base(wn * (GATED ? 32 : 64), lane);
+  const int a_base = SA::base(wm * 32 * W, lane), b_base = SB::base(wn * 32 * W, lane);
 
-  for (int64_t t = xcd_slot(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
+  for (int t = xcd_slot(blockIdx.x, gridDim.x); t < total; t += gridDim.x) {
     int e, mtile, ntile;
     if constexpr (TN) {
-      e = (int)(t / ((int64_t)mtn * ntn));
-      const int rem = (int)(t - (int64_t)e * mtn * ntn);
+      e = t / (mtn * ntn);
+      const int rem = t - e * mtn * ntn;
       mtile = rem / ntn;
       ntile = rem - mtile * ntn;
     } else {
-      e = find_expert(tstart, a.E, (int)t);
+      e = find_expert(tstart, a.E, t);
     }
     const int gbeg = group_begin(a.cu, e, a.M);
     const int rows_e = group_rows(a.cu, e, a.M, gbeg);
     if constexpr (!TN) {
-      const int mte = (rows_e + GA_T - 1) / GA_T;
-      const int lt = (int)t - tstart[e];
+      const int mte = (rows_e + T - 1) / T;
+      const int lt = t - tstart[e];
       ntile = lt / mte;
       mtile = lt - ntile * mte;
     }
-    const int m0 = mtile * GA_T, n0 = ntile * BN;
-    const int mvalid = min(GA_T, (TN ? a.Kd : rows_e) - m0);
+    const int m0 = mtile * T, n0 = ntile * T;
+    const int mvalid = min(T, (TN ? a.Kd : rows_e) - m0);
     const int red = TN ? rows_e : a.Kd;        // length of the reduction
     const int nk = (red + BK - 1) / BK;
-    // source rows of the chunks that this thread loads (KC rows of A)
-    int64_t a_row[GA_CH];
+    // first element of this thread's chunks in stage 0; NULL where the row or column does not exist
+    const mem_t *ap[CH], *bp[CH];
+    int ak[CH], bk[CH];                        // their k in stage 0
 #pragma unroll
-    for (int i = 0; i < GA_CH; ++i) {
-      if constexpr (!TN) {
-        const int r = SA::row(tid + i * GA_THREADS);
-        a_row[i] = -1;
-        if (r < mvalid) {
-          a_row[i] = gbeg + m0 + r;
-          if (a.row_src) {
-            const int src = a.row_src[gbeg + m0 + r];
-            a_row[i] = src < 0 || src / a.a_k >= a.a_rows ? -1 : src / a.a_k;
-          }
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * GA_THREADS;
+      if constexpr (TN) {
+        ak[i] = SA::row(c);
+        const int col = m0 + SA::chunk(c) * EPC;
+        ap[i] = col < a.Kd ? A + (size_t)(gbeg + ak[i]) * a.Kd + col : nullptr;
+      } else {
+        ak[i] = SA::chunk(c) * EPC;
+        const int r = SA::row(c);
+        int64_t row = r < mvalid ? gbeg + m0 + r : -1;
+        if (a.row_src && row >= 0) {
+          const int src = a.row_src[row];
+          row = src < 0 || src / a.a_k >= a.a_rows ? -1 : src / a.a_k;
         }
+        ap[i] = row >= 0 ? A + (size_t)row * a.Kd + ak[i] : nullptr;
+      }
+      if constexpr (BKC) {
+        const int n = n0 + SB::row(c);
+        bk[i] = SB::chunk(c) * EPC;
+        bp[i] = n < a.N ? B + ((size_t)e * a.N + n) * a.Kd + bk[i] : nullptr;
+      } else {
+        bk[i] = SB::row(c);
+        const int col = n0 + SB::chunk(c) * EPC;
+        bp[i] = col < a.N ? B + ((TN ? (size_t)gbeg : (size_t)e * a.Kd) + bk[i]) * a.N + col : nullptr;
       }
     }
-    i32x4_t ra[GA_CH], rb[GA_CH];
-    auto load = [&](int kt) __attribute__((always_inline)) {
+    struct Regs {
+      i32x4_t a[CH], b[CH];
+    };
+    auto load = [&](Regs& r, int kt) __attribute__((always_inline)) {
+      const size_t a_step = (size_t)kt * BK * (AKC ? 1 : a.Kd), b_step = (size_t)kt * BK * (BKC ? 1 : a.N);
 #pragma unroll
-      for (int i = 0; i < GA_CH; ++i) {
-        const int c = tid + i * GA_THREADS;
+      for (int i = 0; i < CH; ++i) {
         const i32x4_t z = {0, 0, 0, 0};
-        ra[i] = rb[i] = z;
-        if constexpr (AKC) {
-          const int k = kt * BK + SA::chunk(c) * EPC;
-          if (a_row[i] >= 0 && k < red) ra[i] = load_chunk<EL>(A + (size_t)a_row[i] * a.Kd + k, red - k);
-        } else {
-          const int k = kt * BK + SA::row(c), col = m0 + SA::chunk(c) * EPC;
-          if (k < red && col < a.Kd) ra[i] = load_chunk<EL>(A + (size_t)(gbeg + k) * a.Kd + col, a.Kd - col);
-        }
-        if constexpr (BKC) {
-          const int r = SB::row(c), k = kt * BK + SB::chunk(c) * EPC;
-          const int n = n0 + (GATED ? r & 63 : r);
-          const mem_t* B = static_cast<const mem_t*>(GATED && r >= 64 ? a.B1 : a.B0);
-          if (n < a.N && k < red) rb[i] = load_chunk<EL>(B + ((size_t)e * a.N + n) * a.Kd + k, red - k);
-        } else {
-          const int k = kt * BK + SB::row(c), col = n0 + SB::chunk(c) * EPC;
-          const size_t brow = TN ? (size_t)(gbeg + k) : (size_t)e * a.Kd + k;
-          if (k < red && col < a.N) rb[i] = load_chunk<EL>(static_cast<const mem_t*>(a.B0) + brow * a.N + col, a.N - col);
+        r.a[i] = r.b[i] = z;
+        if (ap[i] && kt * BK + ak[i] < red) r.a[i] = load_chunk(ap[i] + a_step, a_end);
+        if (bp[i] && kt * BK + bk[i] < red) r.b[i] = load_chunk(bp[i] + b_step, b_end);
+      }
+      if (kt == nk - 1) {  // chunks along the reduction end with it
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          if constexpr (AKC) r.a[i] = first_of_chunk(r.a[i], red - kt * BK - ak[i]);
+          if constexpr (BKC) r.b[i] = first_of_chunk(r.b[i], red - kt * BK - bk[i]);
         }
       }
     };
-    typename EL::acc_t acc[2][2];
+    typename EL::acc_t acc[W][W];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < W; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < W; ++nt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[mt][nt][i] = 0;
-    if (nk > 0) load(0);
-    for (int kt = 0; kt < nk; ++kt) {
-      __syncthreads();  // the stage before has been read
+    Regs regs[PD];
 #pragma unroll
-      for (int i = 0; i < GA_CH; ++i) {
-        *reinterpret_cast<i32x4_t*>(sm + (tid + i * GA_THREADS) * 16) = ra[i];
-        *reinterpret_cast<i32x4_t*>(sm + GA_T * 128 + (tid + i * GA_THREADS) * 16) = rb[i];
-      }
-      __syncthreads();
-      if (kt + 1 < nk) load(kt + 1);
+    for (int p = 0; p < PD; ++p)
+      if (p < nk) load(regs[p], p);
+    __syncthreads();  // the last tile's reads are done
+    for (int k0 = 0; k0 < nk; k0 += PD) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        i32x4_t fa[2], fb[2];
+      for (int p = 0; p < PD; ++p) {
+        const int kt = k0 + p;
+        if (kt >= nk) break;
+        unsigned char* st = smem + (kt & 1) * STAGE;  // its readers of stage kt - 2 all passed the barrier of kt - 1
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) fa[mt] = SA::frag(sm, a_base, mt, kk, lane);
+        for (int i = 0; i < CH; ++i) {
+          *reinterpret_cast<i32x4_t*>(st + (tid + i * GA_THREADS) * 16) = regs[p].a[i];
+          *reinterpret_cast<i32x4_t*>(st + T * 128 + (tid + i * GA_THREADS) * 16) = regs[p].b[i];
+        }
+        __syncthreads();
+        if (kt + PD < nk) load(regs[p], kt + PD);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) fb[nt] = SB::frag(sm + GA_T * 128, b_base, GATED ? 2 * nt : nt, kk, lane);
+        for (int kk = 0; kk < 4; ++kk) {
+          i32x4_t fa[W], fb[W];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < W; ++mt) fa[mt] = SA::frag(st, a_base, mt, kk, lane);
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) EL::mma(acc[mt][nt], fb[nt], fa[mt]);
+          for (int nt = 0; nt < W; ++nt) fb[nt] = SB::frag(st + T * 128, b_base, nt, kk, lane);
+#pragma unroll
+          for (int mt = 0; mt < W; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < W; ++nt) EL::mma(acc[mt][nt], fb[nt], fa[mt]);
+        }
       }
     }
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const int r = wm * 64 + mt * 32 + (lane & 31);
+    for (int mt = 0; mt < W; ++mt) {
+      const int r = wm * 32 * W + mt * 32 + (lane & 31);
       const bool ok = r < mvalid;
       const size_t row = TN ? (size_t)e * a.Kd + m0 + (ok ? r : 0) : (size_t)(gbeg + m0 + (ok ? r : 0));
-      float sa = 1.f;
-      if constexpr (std::is_same<EL, ElI8>::value) {
-        size_t src = row;
-        bool have = ok;
-        if (a.row_src) {
-          const int v = a.row_src[row];
-          have = ok && v >= 0 && v / a.a_k < a.a_rows;
-          src = have ? v / a.a_k : 0;
-        }
-        sa = have ? a.a_sf[src] : 0.f;
-      }
 #pragma unroll
-      for (int nt = 0; nt < (GATED ? 1 : 2); ++nt)
+      for (int nt = 0; nt < W; ++nt)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const int c0 = n0 + wn * (GATED ? 32 : 64) + nt * 32 + 16 * p;
+          const int c0 = n0 + wn * 32 * W + nt * 32 + 16 * p;
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int c = c0 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-            if constexpr (std::is_same<EL, ElI8>::value) {
-              const size_t sb = (size_t)e * a.N + min(c, a.N - 1);
-              v[i] = sa == 0.f ? 0.f : (float)acc[mt][nt][8 * p + i] * sa * a.b_sf0[sb];
-              if constexpr (GATED)
-                v[i] = sa == 0.f ? 0.f : silu_f32(v[i]) * ((float)acc[mt][1][8 * p + i] * sa * a.b_sf1[sb]);
-            } else {
-              v[i] = acc[mt][nt][8 * p + i];
-              if (TN && OUT_F32 && a.accumulate && ok && c < a.N) v[i] += static_cast<const float*>(a.C)[row * a.N + c];
-            }
+            v[i] = acc[mt][nt][8 * p + i];
+            if (TN && OUT_F32 && a.accumulate && ok && c < a.N) v[i] += static_cast<const float*>(a.C)[row * a.N + c];
           }
           store_run<OUT_F32>(a.C, row, a.N, c0, lane, ok, vec, v);
         }
@@ -399,11 +400,26 @@ __global__ __launch_bounds__(GA_THREADS) void gg_any_kernel(GgArgs a) {
   }
 }
 
-// Tiles of a launch are counted in 31 bits by the callers' checks.
-template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED = false>
-moe_status_t launch_gg_any(const GgArgs& a, hipStream_t s) {
-  gg_any_kernel<EL, AKC, BKC, OUT_F32, GATED><<<4 * device_cu_count(), GA_THREADS, 0, s>>>(a);
+template <bool AKC, bool BKC, bool OUT_F32, int T, int PD>
+moe_status_t launch_gg_any_t(const GgArgs& a, hipStream_t s) {
+  constexpr int LDS = 4 * T * 128 + (GG_MAX_E + 1 + GA_THREADS / 64) * 4;
+  static std::atomic<unsigned char> lds_set[MOE_MAX_DEVICES];
+  const auto kernel = &gg_any_kernel<AKC, BKC, OUT_F32, T, PD>;
+  if (ensure_lds_limit(reinterpret_cast<const void*>(kernel), LDS, lds_set) != MOE_OK) return MOE_EHIP;
+  constexpr int PER_CU = 160 * 1024 / LDS;
+  gg_any_kernel<AKC, BKC, OUT_F32, T, PD><<<PER_CU * device_cu_count(), GA_THREADS, LDS, s>>>(a);
   return launch_status();
+}
+
+// Tiles of 128 x 128 where there are two for each CU, else of 64 x 64, us beside each other (64 / 128):
+//   8 experts 2047 x 1023, 100 rows each (64 tiles of 128) 58 / 63; 64 experts, 384 rows each (1792) 447 / 284, dW 776 / 605;
+//   8192 rows, 7167 x 2047 (1024) 760 / 386
+template <bool AKC, bool BKC, bool OUT_F32>
+moe_status_t launch_gg_any(const GgArgs& a, hipStream_t s) {
+  const int64_t groups = !AKC || a.E < a.M ? a.E : a.M;
+  const int64_t down = !AKC ? groups * ((a.Kd + 127) / 128) : groups + (a.M - groups) / 128;
+  if (down * ((a.N + 127) / 128) < 2 * (int64_t)device_cu_count()) return launch_gg_any_t<AKC, BKC, OUT_F32, 64, 3>(a, s);
+  return launch_gg_any_t<AKC, BKC, OUT_F32, 128, AKC ? 2 : 1>(a, s);
 }
 
 }  // namespace moe

@@ -14,8 +14,13 @@ moe_status_t launch(const GgArgs& a, hipStream_t s) {
   // whole 16-byte words along every axis that a load runs along
   const bool words = (size_t)a.Kd * ES % 16 == 0 && (BKC || (size_t)a.N * ES % 16 == 0) && (uintptr_t)a.A % 16 == 0 &&
                      (uintptr_t)a.B0 % 16 == 0;
-  if (!words) return launch_gg_any<EL, AKC, BKC, OUT_F32>(a, s);
-  switch (gg_form(a, !AKC, ES == 4, a.N)) {
+  const GgForm form = gg_form(a, !AKC, ES == 4, a.N);
+  if (!words) {
+    if constexpr (ES == 2) return launch_gg_any<AKC, BKC, OUT_F32>(a, s);
+    else if (form <= GG_THIN) return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, GtThinDw>(a, s);
+    else return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, GtSmallDw>(a, s);
+  }
+  switch (form) {
     case GG_STREAM:  // (not where rows are gathered from no token at all)
       if constexpr (AKC)
         if (!a.row_src || a.a_rows > 0) return launch_gg_stream<EL, BKC, OUT_F32, false>(a, s);

@@ -1,4 +1,4 @@
-// Tiles of the grouped products for rows of whole 16-byte words: both operands go from memory to LDS directly, two stages in
+// Tiles of the grouped products for rows of whole 16-byte words, or in fp32 of any length: both operands go from memory to LDS directly, two stages in
 // turn, and within a wave the loads of the next stage and the fragment reads of the next step are spread between
 // the products of this one, across the stage barrier too.
 //
@@ -15,14 +15,17 @@ namespace moe {
 constexpr int GT_PANEL = 8;
 constexpr int GT_OUT = (int)0x80000000u;  // an offset past every range: loads zeros
 
-template <class EL, int WM_, int WN_, int MT_, int NT_, int NS_ = 2>
+// DW: rows of any length, loaded by the dword (a quarter of the bytes per wave load).
+template <class EL, int WM_, int WN_, int MT_, int NT_, int NS_ = 2, bool DW_ = false>
 struct GtCfg {
   static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
   static constexpr int NS = NS_;  // stages in LDS
+  static constexpr bool DW = DW_;
   static constexpr int W = WM * WN, THREADS = 64 * W;
   static constexpr int BM = WM * MT * 32, BN = WN * NT * 32;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int LDA = BM / (8 * W), LDB = BN / (8 * W);  // wave loads per stage
+  static constexpr int LOAD = DW ? 256 : 1024;                     // bytes of a wave load
+  static constexpr int LDA = A_BYTES / (LOAD * W), LDB = B_BYTES / (LOAD * W);
   static constexpr bool SCALED = std::is_same<EL, ElI8>::value;
   // scales of a tile's rows and columns, twice (gated: both matrices' columns, in runs of 64 at least)
   static constexpr int SC_WAVES = SCALED ? (BM + (BN > 128 ? BN : 128)) / 64 : 0;
@@ -31,7 +34,8 @@ struct GtCfg {
   static constexpr int SCHED = NS * STAGE + 2 * SC_BYTES;
   static constexpr int LDS = SCHED + (GG_MAX_E + 1 + W) * 4;
   static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && (4 * W) % 8 == 0, "whole wave loads, one swizzle per lane");
-  static_assert(BM % 64 == 0 && LDA + LDB <= 31, "whole wave loads of scales; waits count to 63");
+  static_assert(BM % 64 == 0 && (NS - 2) * (LDA + LDB) <= 63, "whole wave loads of scales; waits count to 63");
+  static_assert(!DW || EL::BYTES == 4, "a dword is an element");
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
@@ -64,19 +68,26 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   const uint32_t lds0 = lds_addr(smem);
   const int pitch = Kd * ES, npitch = N * ES;  // bytes of a KC row, of an MC row of B (and pitch: of A, TN)
 
-  // Wave load j = wave + W i fills chunks 64 j .. 64 j + 63 of an operand's stage.
+  // Wave load j = wave + W i fills chunks 64 j .. 64 j + 63 of an operand's stage (DW: dwords 64 j .. 64 j + 63).
+  auto chunk_of = [&](int i) __attribute__((always_inline)) {
+    return CF::DW ? (wave + W * i) * 16 + (lane >> 2) : (wave + W * i) * 64 + lane;
+  };
+  const int sub = CF::DW ? (lane & 3) * 4 : 0;
+  // byte along the row; whole words of a KC operand: the same for every i
+  auto a_byte = [&](int i) __attribute__((always_inline)) { return SA::chunk(chunk_of(AKC && !CF::DW ? 0 : i)) * 16 + sub; };
+  auto b_byte = [&](int i) __attribute__((always_inline)) { return SB::chunk(chunk_of(BKC && !CF::DW ? 0 : i)) * 16 + sub; };
   int a_row[CF::LDA], b_off[CF::LDB];
 #pragma unroll
-  for (int i = 0; i < CF::LDA; ++i) a_row[i] = SA::row((wave + W * i) * 64 + lane);
-  const int a_chunk = SA::chunk(wave * 64 + lane);  // KC: the same for every i
+  for (int i = 0; i < CF::LDA; ++i) a_row[i] = SA::row(chunk_of(i));
 #pragma unroll
   for (int i = 0; i < CF::LDB; ++i) {
-    const int c = (wave + W * i) * 64 + lane;
-    const int r = SB::row(c);
-    if constexpr (BKC) b_off[i] = (GATED ? r % BN : r) * pitch + SB::chunk(c) * 16;
-    else b_off[i] = r * npitch + SB::chunk(c) * 16;
+    const int r = SB::row(chunk_of(i));
+    b_off[i] = BKC ? (GATED ? r % BN : r) * pitch + b_byte(i) : r * npitch + b_byte(i);
   }
-  const int b_chunk = SB::chunk(wave * 64 + lane);
+  auto lds_dma = [&](i32x4_t rsrc, uint32_t to, int voff, int soff) __attribute__((always_inline)) {
+    if constexpr (CF::DW) lds_dma4(rsrc, to, voff, soff);
+    else lds_dma16(rsrc, to, voff, soff);
+  };
 
   struct Tile {
     int e, gbeg, row0, rows_valid, n0, nmt, nk, red;
@@ -128,7 +139,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       d.pA = A + ((size_t)d.gbeg * Kd + d.row0) * ES;
       d.pB = static_cast<const unsigned char*>(a.B0) + ((size_t)d.gbeg * N + d.n0) * ES;
 #pragma unroll
-      for (int i = 0; i < CF::LDA; ++i) d.a_off[i] = a_row[i] * pitch + SA::chunk((wave + W * i) * 64 + lane) * 16;
+      for (int i = 0; i < CF::LDA; ++i) d.a_off[i] = a_row[i] * pitch + a_byte(i);
     } else {
       if (a.row_src) {
         d.rA = make_rsrc(A, (uint32_t)a.a_rows * (uint32_t)pitch);
@@ -140,7 +151,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
 #pragma unroll
         for (int i = 0; i < CF::LDA; ++i) {
           const int at = src[i] / a.a_k;
-          d.a_off[i] = a_row[i] < d.rows_valid && src[i] >= 0 && at < a.a_rows ? at * pitch + a_chunk * 16 : GT_OUT;
+          d.a_off[i] = a_row[i] < d.rows_valid && src[i] >= 0 && at < a.a_rows ? at * pitch + a_byte(i) : GT_OUT;
         }
 #pragma unroll
         for (int i = 0; i < CF::SC_LD; ++i) {
@@ -150,7 +161,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       } else {
         d.rA = make_rsrc(A + (size_t)d.row0 * pitch, (uint32_t)d.rows_valid * (uint32_t)pitch);
 #pragma unroll
-        for (int i = 0; i < CF::LDA; ++i) d.a_off[i] = a_row[i] < d.rows_valid ? a_row[i] * pitch + a_chunk * 16 : GT_OUT;
+        for (int i = 0; i < CF::LDA; ++i) d.a_off[i] = a_row[i] < d.rows_valid ? a_row[i] * pitch + a_byte(i) : GT_OUT;
 #pragma unroll
         for (int i = 0; i < CF::SC_LD; ++i) {
           const int r = (wave + W * i) * 64 + lane;
@@ -180,25 +191,25 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
     constexpr int j = decltype(j_)::value;
     const uint32_t so = lds0 + (uint32_t)buf * CF::STAGE;
     if constexpr (j < CF::LDA) {
-      const uint32_t to = so + (wave + W * j) * 1024;
+      const uint32_t to = so + (wave + W * j) * CF::LOAD;
       if constexpr (AKC) {
-        const bool cut = kt * 128 + a_chunk * 16 >= pitch;  // the row ends inside this stage
-        lds_dma16(d.rA, to, cut ? GT_OUT : d.a_off[j], kt * 128);
+        const bool cut = kt * 128 + a_byte(j) >= pitch;  // the row ends inside this stage
+        lds_dma(d.rA, to, cut ? GT_OUT : d.a_off[j], kt * 128);
       } else {
         // the descriptor begins at this stage's first row and ends with the group: rows past it read as zeros
         const uint32_t rows = (uint32_t)min(BK, d.red - kt * BK);
-        lds_dma16(make_rsrc(d.pA + (size_t)kt * BK * pitch, rows * (uint32_t)pitch - (uint32_t)d.row0 * ES), to, d.a_off[j], 0);
+        lds_dma(make_rsrc(d.pA + (size_t)kt * BK * pitch, rows * (uint32_t)pitch - (uint32_t)d.row0 * ES), to, d.a_off[j], 0);
       }
     } else if constexpr (j < PIECES) {
       constexpr int i = j - CF::LDA;
-      const uint32_t to = so + CF::A_BYTES + (wave + W * i) * 1024;
+      const uint32_t to = so + CF::A_BYTES + (wave + W * i) * CF::LOAD;
       if constexpr (BKC) {
         constexpr bool second = GATED && i >= CF::LDB / 2;
-        const bool cut = kt * 128 + b_chunk * 16 >= pitch;
-        lds_dma16(second ? d.rB1 : d.rB0, to, cut ? GT_OUT : b_off[i], kt * 128);
+        const bool cut = kt * 128 + b_byte(i) >= pitch;
+        lds_dma(second ? d.rB1 : d.rB0, to, cut ? GT_OUT : b_off[i], kt * 128);
       } else {
         const uint32_t rows = (uint32_t)min(BK, d.red - kt * BK);
-        lds_dma16(make_rsrc(d.pB + (size_t)kt * BK * npitch, rows * (uint32_t)npitch - (uint32_t)d.n0 * ES), to, b_off[i], 0);
+        lds_dma(make_rsrc(d.pB + (size_t)kt * BK * npitch, rows * (uint32_t)npitch - (uint32_t)d.n0 * ES), to, b_off[i], 0);
       }
     }
   };
@@ -349,7 +360,8 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       buf = 0;
       const int first = min(NS, cur.nk);
       for (int st = 0; st < first; ++st) load_all(cur, st, st);
-      wait_vm_dyn<(NS - 1) * PIECES>((first - 1) * PIECES);
+      constexpr int MOST = (NS - 1) * PIECES < 63 ? (NS - 1) * PIECES : 63;
+      wait_vm_dyn<MOST>(min((first - 1) * PIECES, MOST));
       asm volatile("s_barrier" ::: "memory");
     }
     if constexpr (TN) {
@@ -444,6 +456,9 @@ template <class EL>
 using GtSmall = GtCfg<EL, 2, 2, 2, 2>;
 template <class EL>
 using GtThin = GtCfg<EL, 4, 1, 1, 2, 4>;
+// fp32 rows of any length. (Large has no registers left for four times the offsets.)
+using GtSmallDw = GtCfg<ElF32, 2, 2, 2, 2, 2, true>;
+using GtThinDw = GtCfg<ElF32, 4, 1, 1, 2, 4, true>;
 
 enum GgForm { GG_STREAM, GG_THIN, GG_SMALL, GG_LARGE };
 
@@ -460,6 +475,7 @@ enum GgForm { GG_STREAM, GG_THIN, GG_SMALL, GG_LARGE };
 //   fp32 [K][N], 8 experts 7168 x 2048 (256): [16] 89 / 260 / 425 / 458  [32] 141 / 260 / 429 / 463  [64] 251 / 262 / 433 / 467
 //   fp32 [K][N], 64 experts 2048 x 1024 (1024): [1] 98 / 303 / 128 / 139  [16] 102 / 303 / 129 / 140
 //   dW, 64 experts 2048 x 24 (384 rows; 1024): - / 22 / 22 / 28, 24 x 2048 (2048): - / 38 / 23 / 34
+//   dW in fp32, 64 experts 2047 x 23 (by the dword): - / 79 / 112
 //   dW, one expert 1024 x 1024 (8192 rows; 128): - / 50 / 87 / 150, 7168 x 2048 (1792): - / 352 / 243 / 204
 inline GgForm gg_form(const GgArgs& a, bool tn, bool f32, int columns) {
   const int64_t cus = device_cu_count();
@@ -475,9 +491,8 @@ inline GgForm gg_form(const GgArgs& a, bool tn, bool f32, int columns) {
     if (a.M <= 32 * slots && (f32 ? 1 : 4) * thin <= cus) return GG_STREAM;
     if (a.M <= 64 * slots && 8 * thin <= cus) return GG_STREAM;
   }
-  if (thin <= 2 * cus || (!tn && columns <= 64)) return GG_THIN;
-  const bool narrow = columns <= 64 || (tn && a.Kd <= 64);
-  return !narrow && (tn || a.M > 128 * slots) && 4 * tiles(256, 256) >= 3 * cus ? GG_LARGE : GG_SMALL;
+  if (thin <= 2 * cus || columns <= 64) return GG_THIN;
+  return !(tn && a.Kd <= 64) && (tn || a.M > 128 * slots) && 4 * tiles(256, 256) >= 3 * cus ? GG_LARGE : GG_SMALL;
 }
 
 template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED, class CF>
