@@ -19,25 +19,42 @@ __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
   return s < 0x1p-120f ? 0x1p-120f : s;
 }
 
-// x / s by one product with inv = fl32(1 / s) is off by less than 2^-14 (|x / s| <= 127.01, three
-// roundings of 2^-24): only a quotient that lands within 2^-13 of a half step can round the wrong
-// way. There the border b = n + 1/2 is compared with x itself: b s has at most 32 significant
-// bits and fma rounds once, so the sign of x - b s is exact.
-__device__ __forceinline__ float int8_code(float x, float s, float inv) {
-  const float v = x * inv;
-  float r = __builtin_rintf(v);
-  const float d = v - r;
-  if (__builtin_fabsf(d) > 0.5f - 0x1p-13f) {
-    const float b = r + __builtin_copysignf(0.5f, d);
-    const float e = __builtin_fmaf(-b, s, x);
-    r = e > 0.f ? b + 0.5f : e < 0.f ? b - 0.5f : 2.0f * __builtin_rintf(0.5f * b);
+// Codes of n values with their scales s and inv = fl32(1 / s), as the low bytes of code[].
+// x inv, rounded once to an integer by the addition of 1.5 * 2^23 (whose low byte is then the code), is off from x / s by less than
+// 2^-16 (|x / s| <= 127.01, inv by 2^-24 of it): only a quotient within 2^-13 of a half step can round the wrong way.
+// There the border b = n + 1/2 is compared with x itself: b s has at most 32 significant bits and fma rounds once, so the sign
+// of x - b s is exact. `bad`: some inv is 0, a column with a NaN or an infinity, whose codes are 0.
+template <int N, int NS>
+__device__ __forceinline__ void int8_codes(const float (&x)[N], const float (&s)[NS], const float (&inv)[NS], bool bad,
+                                           uint32_t (&code)[N]) {
+  constexpr float M = 12582912.0f;
+  float off = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float t = __builtin_fmaf(x[i], inv[i % NS], M);
+    code[i] = __float_as_uint(t);
+    off = __builtin_fmaxf(off, __builtin_fabsf(__builtin_fmaf(x[i], inv[i % NS], -(t - M))));
   }
-  return r;
+  if (bad || off > 0.5f - 0x1p-13f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float si = s[i % NS], ii = inv[i % NS];
+      float r = __uint_as_float(code[i]) - M;
+      const float d = __builtin_fmaf(x[i], ii, -r);
+      if (__builtin_fabsf(d) > 0.5f - 0x1p-13f) {
+        const float b = r + __builtin_copysignf(0.5f, d);
+        const float e = __builtin_fmaf(-b, si, x[i]);
+        r = e > 0.f ? b + 0.5f : e < 0.f ? b - 0.5f : 2.0f * __builtin_rintf(0.5f * b);
+      }
+      code[i] = ii == 0.f ? 0u : __float_as_uint(r + M);
+    }
+  }
 }
 
-__device__ __forceinline__ uint32_t pack_i8x4(float a, float b, float c, float d) {
-  return ((uint32_t)(int)a & 0xffu) | ((uint32_t)(int)b & 0xffu) << 8 | ((uint32_t)(int)c & 0xffu) << 16 |
-         (uint32_t)(int)d << 24;
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u),
+                               0x05040100u);
 }
 
 __device__ __forceinline__ float i8_at(uint32_t w, int i) { return (float)((int)(w << (24 - 8 * i)) >> 24); }
