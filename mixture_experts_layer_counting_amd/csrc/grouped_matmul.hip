@@ -14,7 +14,7 @@ moe_status_t launch(const GgArgs& a, hipStream_t s) {
   // whole 16-byte words along every axis that a load runs along
   const bool words = (size_t)a.Kd * ES % 16 == 0 && (BKC || (size_t)a.N * ES % 16 == 0) && (uintptr_t)a.A % 16 == 0 &&
                      (uintptr_t)a.B0 % 16 == 0;
-  const GgForm form = gg_form(a, !AKC, ES == 4, a.N);
+  const GgForm form = gg_form(a, !AKC, BKC, ES == 4, a.N);
   if (!words) {
     if constexpr (ES == 2) return launch_gg_any<AKC, BKC, OUT_F32>(a, s);
     else if (form <= GG_THIN) return launch_gg_tiles<EL, AKC, BKC, OUT_F32, false, GtThinDw>(a, s);

@@ -91,7 +91,6 @@ __global__ __launch_bounds__(GS_THREADS) void gg_stream_kernel(GgArgs a, int ks)
   const int n0 = cb * BN + wl / ks * WC;        // the wave's first column
   const size_t pitch = (size_t)Kd * ES, npitch = (size_t)N * ES;
   const int steps = (int)((pitch + KB - 1) / KB);
-  const int first = (int)((int64_t)steps * slice / ks), last = (int)((int64_t)steps * (slice + 1) / ks);
   const unsigned char* B = static_cast<const unsigned char*>(GATED && wave >= WM ? a.B1 : a.B0);
   // columns past the last read another one's values; their results are not stored
   const unsigned char* wp;
@@ -183,12 +182,13 @@ __global__ __launch_bounds__(GS_THREADS) void gg_stream_kernel(GgArgs a, int ks)
     }
   };
   Step s0, s1;
-  if (first < last) load(s0, first);
-  for (int it = first; it < last; it += 2) {
-    if (it + 1 < last) load(s1, it + 1);
+  // slice s takes every ks-th step: the waves of a block read neighbouring lines
+  if (slice < steps) load(s0, slice);
+  for (int it = slice; it < steps; it += 2 * ks) {
+    if (it + ks < steps) load(s1, it + ks);
     mul(s0);
-    if (it + 2 < last) load(s0, it + 2);
-    if (it + 1 < last) mul(s1);
+    if (it + 2 * ks < steps) load(s0, it + 2 * ks);
+    if (it + ks < steps) mul(s1);
   }
 
   // lane l holds row l % 16 and the columns 4 G + c (weights [N][K]) or 16 G + 4 c + i ([K][N]) of the wave's
@@ -233,13 +233,14 @@ moe_status_t launch_gg_stream(const GgArgs& a, hipStream_t s) {
   const int64_t slots = a.M < a.E ? a.M : a.E;  // at most so many experts have rows
   // n experts with R rows make at most n + (R - n) / 16 chunks; blocks past the last one have none
   const int64_t chunks = slots + (a.M - slots) / 16;
-  // Slices of the reduction: as many as leave 16 waves a CU. Measured, us, by 8 / 4 / 2 / 1 slices (gated: 4 / 2 / 1):
-  //   INT8 1 x 7168 x 2048 (128 waves unsplit) 7.5 / 11.5 / 19 / 35; 8 experts 7168 x 2048 (1024) 24.5 / 24.2 / 23.9 / 39
-  //   8 experts 2048 x 7168 (3584) 37 / 31 / 26 / 25; gate/up, 8 experts 7168 x 2048 (2048) 41 / 40 / 41
-  //   bf16 [K][N], 8 experts 7168 x 2048 (256) 37 / 52 / 99 / 191; fp32, 64 experts 2048 x 1024 (1024) 101 / 98 / - / 153
-  const int64_t waves = chunks * ((a.N + WC - 1) / WC) * (GATED ? 2 : 1);
+  // Slices of the reduction: as many as leave 8 waves a CU (fp32, whose products take longer: 16). Measured, us, by 8 / 4 / 2 / 1
+  // slices, weights not in a cache (gated: 4 / 2 / 1): INT8 1 x 7168 x 2048 (128 waves unsplit) 7 / 11 / 18 / 33; gate/up, 8 experts
+  // 7168 x 2048 (2048) 57 / 58 / 50; bf16 [K][N], 8 experts 7168 x 2048 (256) 44 / 68 / 125 / 243. In a cache: INT8, 8 experts
+  // 7168 x 2048 (1024) 24.5 / 24.2 / 23.9 / 39, 2048 x 7168 (3584) 37 / 31 / 26 / 25; fp32, 64 experts 2048 x 1024 (1024) 101 / 98 / - / 153.
+  // (counted for evenly filled groups)
+  const int64_t waves = slots * (((a.M + slots - 1) / slots + 15) / 16) * ((a.N + WC - 1) / WC) * (GATED ? 2 : 1);
   int ks = WM;
-  while (ks > 1 && waves * ks > 16 * (int64_t)device_cu_count()) ks /= 2;
+  while (ks > 1 && waves * ks > (EL::BYTES == 4 ? 16 : 8) * (int64_t)device_cu_count()) ks /= 2;
   const int BN = WM / ks * WC;
   const unsigned blocks = (unsigned)(chunks * ((a.N + BN - 1) / BN));
   gg_stream_kernel<EL, BKC, OUT_F32, GATED><<<blocks, GS_THREADS, 0, s>>>(a, ks);

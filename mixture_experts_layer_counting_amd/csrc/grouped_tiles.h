@@ -487,7 +487,8 @@ enum GgForm { GG_STREAM, GG_THIN, GG_SMALL, GG_LARGE };
 // where gated) and the rows per group. Measured on 256 CUs, us, stream / thin / small / large, rows per group in brackets:
 //   INT8, dense 7168 x 2048 (32 thin tiles): [1] 7.5 / 23 / 35 / 50  [16] 10 / 23 / 36 / 50  [64] 16 / 23 / 38 / 54
 //                                           [128] 30 / 25 / 43 / 54  [2048, 512 tiles] - / 50 / 58 / 99  [4096] - / 130 / 62 / 103
-//   INT8, 8 experts 7168 x 2048 (256): [1] 24 / 24 / 49 / 57  [16] 31 / 25 / 50 / 57  [128] 200 / 27 / 62 / 67
+//   INT8, 8 experts 7168 x 2048 (256): [1] 22 / 24 / 49 / 57  [8] 25 / 24 / 49 / 57  [16] 32 / 25 / 50 / 57  [128] 200 / 27 / 62 / 67
+//   bf16 [N][K], the same: [1] 39 / 42 / 92 / 104  [8] 44 / 42 / 92 / 105  [16] 58 / 43 / 92 / 105; 16 experts 1024 x 512 (128): [16] 7 / 9 / 17 / 19
 //   INT8 gate/up, the same (512): [1] 40 / 49 / 63 / 67  [8] 47 / 49 / 63 / 67  [16] 57 / 49 / 64 / 67
 //   INT8, 8 experts 2048 x 7168 (896): [1] 25 / 34 / 22 / 24  [16] 35 / 33 / 23 / 25
 //   bf16 [K][N], 8 experts 7168 x 2048 (256): [1] 37 / 44 / 93 / 103  [16] 39 / 44 / 94 / 102  [128] 158 / 48 / 110 / 115
@@ -498,7 +499,8 @@ enum GgForm { GG_STREAM, GG_THIN, GG_SMALL, GG_LARGE };
 //   dW, 64 experts 2048 x 24 (384 rows; 1024): - / 22 / 22 / 28, 24 x 2048 (2048): - / 38 / 23 / 34
 //   dW in fp32, 64 experts 2047 x 23 (by the dword): - / 79 / 112
 //   dW, one expert 1024 x 1024 (8192 rows; 128): - / 50 / 87 / 150, 7168 x 2048 (1792): - / 352 / 243 / 204
-inline GgForm gg_form(const GgArgs& a, bool tn, bool f32, int columns) {
+// (weights [N][K], whose rows x come with every 16 columns, stop streaming earlier: `kc`)
+inline GgForm gg_form(const GgArgs& a, bool tn, bool kc, bool f32, int columns) {
   const int64_t cus = device_cu_count();
   const int64_t slots = tn || a.E < a.M ? a.E : a.M;  // at most so many groups have rows
   auto tiles = [&](int bm, int bn) -> int64_t {
@@ -507,7 +509,7 @@ inline GgForm gg_form(const GgArgs& a, bool tn, bool f32, int columns) {
   };
   const int64_t thin = tiles(128, 64);
   if (!tn) {
-    if (a.M <= 16 * slots && thin <= (f32 ? 4 : 1) * cus) return GG_STREAM;
+    if (a.M <= 16 * slots && (f32 ? thin <= 4 * cus : (kc ? 2 : 1) * thin <= cus)) return GG_STREAM;
     if (a.M <= 8 * slots && thin <= 2 * cus) return GG_STREAM;
     if (a.M <= 32 * slots && (f32 ? 1 : 4) * thin <= cus) return GG_STREAM;
     if (a.M <= 64 * slots && 8 * thin <= cus) return GG_STREAM;

@@ -9,7 +9,7 @@ namespace {
 
 template <bool OUT_F32, bool GATED>
 moe_status_t launch(const GgArgs& a, hipStream_t s) {
-  switch (gg_form(a, false, false, GATED ? 2 * a.N : a.N)) {
+  switch (gg_form(a, false, true, false, GATED ? 2 * a.N : a.N)) {
     case GG_STREAM:  // (not where rows are gathered from no token at all)
       if (!a.row_src || a.a_rows > 0) return launch_gg_stream<ElI8, true, OUT_F32, GATED>(a, s);
       [[fallthrough]];
