@@ -4,8 +4,16 @@
 //
 // A block of WM x WN waves, each with MT x NT blocks of 32 x 32. A wave's row blocks lie WM * 32 rows apart, so that
 // the padded rows of a group's last tile fall on all waves alike; a wave skips the blocks that lie wholly past the rows.
-// The persistent loop never waits for its stores: the next tile's first stage is loaded under the last stage of
-// this one and waited for before the stores go out, so its first products need the barrier only.
+// The next tile's first stage is loaded under the last stage of this one and waited for before the stores go out, so that its
+// first products need a barrier only; the stores have until its second stage.
+//
+// What bounds it, 256 x 256 tiles. 8192^3: INT8 2.50 POP/s (a library's product 1.96), bf16 1.33 PFLOP/s (1.19 with the weights [K][N], 1.50
+// with [N][K]): the matrix cores are busy for 69 and 75 % of the cycles, at 1.7 GHz: the power limit. 65536 rows over 52 experts, us:
+// 7168 x 2048 INT8 867 (2.2 POP/s), bf16 1650-1680 (1.16 PFLOP/s); 2048 x 7168 INT8 1030 (1.9), bf16 1730; gate/up INT8 1700.
+// With 384 rows per expert (64 experts, 2048 x 1024) weights, rows and results, 419 MB, bound it: bf16 122 us (3.4 TB/s), INT8 62.
+// dW: 65536 rows over 52 experts, 2048 x 7168 2.05 ms; without its 3 GB of stores 1.55: the tile's 256 KB leave its CU at the rate at
+// which all CUs together fill the memory (5.5 TB/s), and its waves' loads wait behind them (one counter counts both, in order).
+// Two blocks of 256 x 128 with half the stage, one computing while the other stores: 2.27; blocks started out of phase: no change.
 #pragma once
 
 #include "grouped_gemm.h"
@@ -14,6 +22,31 @@ namespace moe {
 
 constexpr int GT_PANEL = 8;
 constexpr int GT_OUT = (int)0x80000000u;  // an offset past every range: loads zeros
+
+// A 32 x 32 block of fp32 whose lane l holds row l % 32 and, in v[4 j + c], column 8 j + 4 (l / 32) + c, to rows of whole 16-byte words, turned
+// through 4.5 KB of LDS that no other wave uses: eight lanes then hold the 128 bytes of a row. `rows`: how many of the 32 there
+// are; p: the first one's first column; `left`: columns from there on. All lanes must be active.
+// A store then writes whole lines, 1 KB in all: dW, 64 experts of 384 rows, 2048 x 1024 188 -> 179 us beside a column per lane and 4 bytes
+// (64 rows over 64 experts, nothing but stores, 97 -> 102).
+constexpr int GT_TURN = 32 * 144;  // rows of 128 bytes, 16 apart: neighbours begin on other banks
+__device__ __forceinline__ void store_turned(unsigned char* turn, float* p, int N, int rows, int left, int lane, bool add,
+                                             const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<f32x4_t*>(turn + (lane & 31) * 144 + 32 * j + 16 * (lane >> 5)) =
+        f32x4_t{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+  const int c = 4 * (lane & 7);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    f32x4_t u = *reinterpret_cast<const f32x4_t*>(turn + r * 144 + 4 * c);
+    if (r < rows && c < left) {
+      f32x4_t* to = reinterpret_cast<f32x4_t*>(p + (size_t)r * N + c);
+      if (add) u += *to;
+      *to = u;
+    }
+  }
+}
 
 // DW: rows of any length, loaded by the dword (a quarter of the bytes per wave load).
 template <class EL, int WM_, int WN_, int MT_, int NT_, int NS_ = 2, bool DW_ = false>
@@ -46,8 +79,9 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   constexpr int BN = GATED ? CF::BN / 2 : CF::BN;  // columns per matrix
   constexpr int SCN = BN < 64 ? 64 : BN;           // and their places among the scales
   constexpr int NS = CF::NS;
-  // fp32 gradients leave with a column per lane, 128 neighbouring bytes of two rows a store
-  constexpr bool COL_LANES = TN && OUT_F32;
+  // fp32 gradients whose rows are not whole words leave with a column per lane, 128 neighbouring bytes of two rows a store
+  constexpr bool COL_LANES = TN && CF::DW;
+  static_assert(W * GT_TURN <= CF::STAGE, "a wave's share of a stage");
   using SA = Staged<EL, AKC, BM>;
   using SB = Staged<EL, BKC, CF::BN>;
   constexpr int BK = SA::BK, ES = EL::BYTES;
@@ -419,6 +453,9 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       continue;
     }
     const float* sc = reinterpret_cast<const float*>(smem + NS * CF::STAGE + par * CF::SC_BYTES);
+    // the stage that is not the next tile's first, once every wave has read it
+    unsigned char* turn = smem + (NS == 2 ? buf ^ 1 : 0) * CF::STAGE + wave * GT_TURN;
+    if (OUT_F32 && vec) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (!TN && mt >= cur.nmt) break;
@@ -431,6 +468,23 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       for (int nt = 0; nt < (GATED ? NT / 2 : NT); ++nt) {
         const int cw = wn * (GATED ? NT / 2 : NT) * 32 + nt * 32;  // inside the tile
         if (cur.n0 + cw >= N) break;
+        if constexpr (OUT_F32) {
+          if (vec) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              v[i] = (float)acc[mt][nt][i];
+              if constexpr (CF::SCALED) {  // a padding row is zeros whatever the weights' scales hold
+                v[i] = v[i] * sa * sc[BM + cw + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)];
+                if (sa == 0.f) v[i] = 0.f;
+              }
+            }
+            const size_t row0 = (TN ? (size_t)cur.e * Kd : 0) + cur.row0 + (r - (lane & 31));
+            store_turned(turn, static_cast<float*>(a.C) + row0 * N + cur.n0 + cw, N, cur.rows_valid - (r - (lane & 31)),
+                         N - cur.n0 - cw, lane, TN && a.accumulate, v);
+            continue;
+          }
+        }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           float v[8];
