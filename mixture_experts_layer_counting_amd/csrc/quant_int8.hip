@@ -7,7 +7,10 @@
 //  weights:  w [E, K, N] (reduction first) -> q [E, N, K], sf [E, N]. The maximum of a column needs all
 //            of K before the first code, so the values are read twice; codes are turned through LDS
 //            and written in runs along k.
-// All are bound by HBM. Any C, K and N: rows may start at any element, whole 16-byte words are
+// All are bound by HBM (a large copy reaches 4.8 TB/s here): rows 8191 x 7168 bf16 34 us, 5.2 TB/s, and back 26.5; 65536 x 2048
+// 69; weights 64 x 2048 x 1024 fp32 212-220 us, 5.6 TB/s over both reads, and back to bf16 90; 52 x 7168 x 2048 bf16 790-805, and
+// back 447-467. The second read of the weights costs a third to a half of a call that is made once per weight: values that stay in registers
+// between the passes would need a whole column's reduction per block. Any C, K and N: rows may start at any element, whole 16-byte words are
 // loaded where they lie inside the row and single elements at its end.
 #include "int8.h"
 #include "tile_sched.h"
