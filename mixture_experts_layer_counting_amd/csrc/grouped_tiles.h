@@ -11,7 +11,7 @@
 // with [N][K]): the matrix cores are busy for 69 and 75 % of the cycles, at 1.7 GHz: the power limit. 65536 rows over 52 experts, us:
 // 7168 x 2048 INT8 867 (2.2 POP/s), bf16 1650-1680 (1.16 PFLOP/s); 2048 x 7168 INT8 1030 (1.9), bf16 1730; gate/up INT8 1700.
 // With 384 rows per expert (64 experts, 2048 x 1024) weights, rows and results, 419 MB, bound it: bf16 122 us (3.4 TB/s), INT8 62.
-// dW: 65536 rows over 52 experts, 2048 x 7168 2.05 ms; without its 3 GB of stores 1.55: the tile's 256 KB leave its CU at the rate at
+// dW: 65536 rows over 52 experts, 2048 x 7168 2.0 ms; without its 3 GB of stores 1.55: the tile's 256 KB leave its CU at the rate at
 // which all CUs together fill the memory (5.5 TB/s), and its waves' loads wait behind them (one counter counts both, in order).
 // Two blocks of 256 x 128 with half the stage, one computing while the other stores: 2.27; blocks started out of phase: no change.
 #pragma once
@@ -28,7 +28,11 @@ constexpr int GT_OUT = (int)0x80000000u;  // an offset past every range: loads z
 // are; p: the first one's first column; `left`: columns from there on. All lanes must be active.
 // A store then writes whole lines, 1 KB in all: dW, 64 experts of 384 rows, 2048 x 1024 188 -> 179 us beside a column per lane and 4 bytes
 // (64 rows over 64 experts, nothing but stores, 97 -> 102).
+// PAST: the stores ask the caches not to keep them. For weight gradients, which outgrow the caches and are read much later, where
+// rows are whole lines (us, kept / past, operands read again): 64 experts 2048 x 1024 179 / 149, 8 of 4096 x 4096 311 / 279, 52 of 2048 x
+// 7168 2076 / 2027; rows that share lines the other way, 2048 x 1000 231 / 257.
 constexpr int GT_TURN = 32 * 144;  // rows of 128 bytes, 16 apart: neighbours begin on other banks
+template <bool PAST>
 __device__ __forceinline__ void store_turned(unsigned char* turn, float* p, int N, int rows, int left, int lane, bool add,
                                              const float (&v)[16]) {
 #pragma unroll
@@ -43,7 +47,8 @@ __device__ __forceinline__ void store_turned(unsigned char* turn, float* p, int 
     if (r < rows && c < left) {
       f32x4_t* to = reinterpret_cast<f32x4_t*>(p + (size_t)r * N + c);
       if (add) u += *to;
-      *to = u;
+      if constexpr (PAST) __builtin_nontemporal_store(u, to);
+      else *to = u;
     }
   }
 }
@@ -72,7 +77,7 @@ struct GtCfg {
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
-template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED, class CF>
+template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED, class CF, bool PAST = false>
 __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   constexpr bool TN = !AKC;
   constexpr int W = CF::W, BM = CF::BM, MT = CF::MT, NT = CF::NT;
@@ -480,7 +485,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
               }
             }
             const size_t row0 = (TN ? (size_t)cur.e * Kd : 0) + cur.row0 + (r - (lane & 31));
-            store_turned(turn, static_cast<float*>(a.C) + row0 * N + cur.n0 + cw, N, cur.rows_valid - (r - (lane & 31)),
+            store_turned<PAST>(turn, static_cast<float*>(a.C) + row0 * N + cur.n0 + cw, N, cur.rows_valid - (r - (lane & 31)),
                          N - cur.n0 - cw, lane, TN && a.accumulate, v);
             continue;
           }
@@ -572,13 +577,18 @@ inline GgForm gg_form(const GgArgs& a, bool tn, bool kc, bool f32, int columns) 
   return !(tn && a.Kd <= 64) && (tn || a.M > 128 * slots) && 4 * tiles(256, 256) >= 3 * cus ? GG_LARGE : GG_SMALL;
 }
 
-template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED, class CF>
+template <class EL, bool AKC, bool BKC, bool OUT_F32, bool GATED, class CF, bool PAST = false>
 moe_status_t launch_gg_tiles(const GgArgs& a, hipStream_t s) {
+  if constexpr (!AKC && OUT_F32 && !CF::DW && !PAST) {
+    // weight gradients whose rows are whole lines
+    if (a.N % 32 == 0 && reinterpret_cast<uintptr_t>(a.C) % 128 == 0)
+      return launch_gg_tiles<EL, AKC, BKC, OUT_F32, GATED, CF, true>(a, s);
+  }
   static std::atomic<unsigned char> lds_set[MOE_MAX_DEVICES];
-  const auto kernel = &gg_tile_kernel<EL, AKC, BKC, OUT_F32, GATED, CF>;
+  const auto kernel = &gg_tile_kernel<EL, AKC, BKC, OUT_F32, GATED, CF, PAST>;
   if (ensure_lds_limit(reinterpret_cast<const void*>(kernel), CF::LDS, lds_set) != MOE_OK) return MOE_EHIP;
   constexpr int PER_CU = 160 * 1024 / CF::LDS < 1024 / CF::THREADS ? 160 * 1024 / CF::LDS : 1024 / CF::THREADS;
-  gg_tile_kernel<EL, AKC, BKC, OUT_F32, GATED, CF><<<PER_CU * device_cu_count(), CF::THREADS, CF::LDS, s>>>(a);
+  gg_tile_kernel<EL, AKC, BKC, OUT_F32, GATED, CF, PAST><<<PER_CU * device_cu_count(), CF::THREADS, CF::LDS, s>>>(a);
   return launch_status();
 }
 
