@@ -29,8 +29,8 @@ constexpr int GT_OUT = (int)0x80000000u;  // an offset past every range: loads z
 // A store then writes whole lines, 1 KB in all: dW, 64 experts of 384 rows, 2048 x 1024 188 -> 179 us beside a column per lane and 4 bytes
 // (64 rows over 64 experts, nothing but stores, 97 -> 102).
 // PAST: the stores ask the caches not to keep them. For weight gradients, which outgrow the caches and are read much later, where
-// rows are whole lines (us, kept / past, operands read again): 64 experts 2048 x 1024 179 / 149, 8 of 4096 x 4096 311 / 279, 52 of 2048 x
-// 7168 2076 / 2027; rows that share lines the other way, 2048 x 1000 231 / 257.
+// rows are whole lines (us, kept / past, operands read again): 64 experts 2048 x 1024 179 / 152, 8 of 4096 x 4096 307 / 275, 52 of 2048 x
+// 7168 2059 / 2019; rows that share lines the other way, 2048 x 1000 231 / 257.
 constexpr int GT_TURN = 32 * 144;  // rows of 128 bytes, 16 apart: neighbours begin on other banks
 template <bool PAST>
 __device__ __forceinline__ void store_turned(unsigned char* turn, float* p, int N, int rows, int left, int lane, bool add,
