@@ -507,7 +507,8 @@ MOE_API moe_status_t moe_dequantize_int8(const int8_t* q, const float* sf, int32
 /* Stacked weights to INT8 with a scale per output column ("Mixture of Kittens", Step 8: the weights are
  * pre-quantised once): w [E, K, N] of w_dtype (BF16 or F32), K the reduction: the layout of the bf16 and fp32
  * experts; q [E, N, K] out (reduction-contiguous), sf [E, N] out. Any K and N with K * N < 2^40;
- * alignment of the elements only. Two kernel launches. */
+ * alignment of the elements only. K = 0: no codes (w and q are not used), scales of 1 where sf is given.
+ * Two kernel launches (one for K = 0). */
 MOE_API moe_status_t moe_quantize_int8_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K, int32_t N,
                                                int8_t* q, float* sf, hipStream_t stream);
 

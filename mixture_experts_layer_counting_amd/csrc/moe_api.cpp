@@ -524,8 +524,9 @@ static moe_status_t check_int8_weights(moe_dtype_t dt, int E, int K, int N) {
 moe_status_t moe_quantize_int8_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K, int32_t N, int8_t* q,
                                        float* sf, hipStream_t stream) {
   const moe_status_t st = check_int8_weights(w_dtype, E, K, N);
-  if (st != MOE_OK || E == 0 || K == 0 || N == 0) return st;
-  if (!w || !q || !sf || !aligned_to(w, elem_bytes(w_dtype)) || !aligned_to(sf, 4)) return MOE_EINVAL;
+  if (st != MOE_OK || E == 0 || N == 0) return st;
+  if (K == 0 && !sf) return MOE_OK;  // no codes, and the scales are not asked for
+  if ((K > 0 && (!w || !q)) || !sf || !aligned_to(w, elem_bytes(w_dtype)) || !aligned_to(sf, 4)) return MOE_EINVAL;
   return launch_quantize_int8_weights(w, w_dtype, E, K, N, q, sf, stream);
 }
 

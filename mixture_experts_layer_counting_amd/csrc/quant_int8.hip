@@ -415,7 +415,7 @@ moe_status_t quantize_weights(const XT* w, int E, int K, int N, int8_t* q, float
   const int64_t slabs = (int64_t)E * ncb;
   weight_scales_i8_kernel<XT><<<grid_of(slabs), 1024, 0, s>>>(w, K, N, ncb, slabs, sf);
   const moe_status_t st = launch_status();
-  if (st != MOE_OK) return st;
+  if (st != MOE_OK || K == 0) return st;
   const int ny = (K + QW_K - 1) / QW_K;
   quant_weights_i8_kernel<XT><<<grid_of(slabs * ny), QW_THREADS, 0, s>>>(w, K, N, ncb, ny, slabs * ny, sf, q);
   return launch_status();

@@ -45,6 +45,14 @@ def test_int8_weights():
         assert status(d, None, None, e, k, n, None, F32, 0) == OK
 
 
+def test_int8_weights_of_an_empty_reduction_have_scales():
+    """K = 0 has no codes, but N scales for each matrix: a pointer for them is checked like any other."""
+    q = moe.moe_quantize_int8_weights
+    for sf in (P + 1, P + 2):
+        assert status(q, None, F32, 2, 0, 8, None, sf, 0) == INVAL
+    assert status(q, None, F32, 2, 0, 0, None, P + 2, 0) == OK and status(q, None, F32, 0, 0, 8, None, P + 2, 0) == OK
+
+
 def test_matmul_int8():
     f = lambda x=P, xs=P, M=8, H=64, N=8, w=P, ws=P, y=P, out=BF16: status(  # noqa: E731
         moe.moe_matmul_int8, x, xs, M, H, N, w, ws, y, out, 0)

@@ -107,6 +107,17 @@ def test_quantize_weights_and_back(E, K, N, dtype):
         assert bool((vg == 9.0).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,N", [(1, 1), (3, 7), (2, 200)])
+def test_weights_of_an_empty_reduction(E, N, dtype):
+    """The largest magnitude of a column without values is 0: its scale is 1. Nothing else is read or written."""
+    sf, sg = guarded((E, N), torch.float32, 9.0)
+    moe.moe_quantize_int8_weights(None, FMT[dtype][0], E, 0, N, None, sf)
+    moe.moe_dequantize_int8_weights(None, sf, E, 0, N, None, FMT[dtype][0])
+    torch.cuda.synchronize()
+    assert bool((sf == 1.0).all()) and bool((sg == 9.0).all())
+
+
 # ----------------------------------------------------------------------------- products
 
 class Groups:
