@@ -506,13 +506,13 @@ MOE_API moe_status_t moe_dequantize_int8(const int8_t* q, const float* sf, int32
 
 /* Stacked weights to INT8 with a scale per output column ("Mixture of Kittens", Step 8: the weights are
  * pre-quantised once): w [E, K, N] of w_dtype (BF16 or F32), K the reduction: the layout of the bf16 and fp32
- * experts; q [E, N, K] out (reduction-contiguous), sf [E, N] out. Any K and N with K * N < 2^40;
- * alignment of the elements only. K = 0: no codes (w and q are not used), scales of 1 where sf is given.
- * Two kernel launches (one for K = 0). */
+ * experts; q [E, N, K] out (reduction-contiguous), sf [E, N] out. Any K and N up to 2^30 with
+ * K * N < 2^40 (MOE_EUNSUPPORTED); alignment of the elements only. K = 0: no codes (w and q are not used), scales
+ * of 1 where sf is given. Two kernel launches (one for K = 0). */
 MOE_API moe_status_t moe_quantize_int8_weights(const void* w, moe_dtype_t w_dtype, int32_t E, int32_t K, int32_t N,
                                                int8_t* q, float* sf, hipStream_t stream);
 
-/* The values of INT8 weights: out [E, K, N] = fl32(q * sf), rounded to out_dtype (BF16 or F32). */
+/* The values of INT8 weights: out [E, K, N] = fl32(q * sf), rounded to out_dtype (BF16 or F32). Sizes as above. */
 MOE_API moe_status_t moe_dequantize_int8_weights(const int8_t* q, const float* sf, int32_t E, int32_t K, int32_t N,
                                                  void* out, moe_dtype_t out_dtype, hipStream_t stream);
 

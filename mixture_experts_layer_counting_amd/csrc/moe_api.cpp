@@ -515,9 +515,10 @@ moe_status_t moe_dequantize_int8(const int8_t* q, const float* sf, int32_t R, in
   return launch_dequantize_int8(q, sf, R, C, out, out_dtype, stream);
 }
 
+// The kernels step along K and N in 32 bits, by at most 1024 past the end.
 static moe_status_t check_int8_weights(moe_dtype_t dt, int E, int K, int N) {
   if (E < 0 || K < 0 || N < 0) return MOE_EINVAL;
-  if (!f32_or_bf16(dt) || (int64_t)K * N >= 1ll << 40) return MOE_EUNSUPPORTED;
+  if (!f32_or_bf16(dt) || K > 1 << 30 || N > 1 << 30 || (int64_t)K * N >= 1ll << 40) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 

@@ -53,6 +53,18 @@ def test_int8_weights_of_an_empty_reduction_have_scales():
     assert status(q, None, F32, 2, 0, 0, None, P + 2, 0) == OK and status(q, None, F32, 0, 0, 8, None, P + 2, 0) == OK
 
 
+def test_int8_weights_past_what_the_kernels_count():
+    """Rows and columns are counted in 32 bits, up to a step past the last one."""
+    q, d = moe.moe_quantize_int8_weights, moe.moe_dequantize_int8_weights
+    top = 2 ** 30
+    for k, n in ((top + 1, 1), (1, top + 1), (2 ** 31 - 1, 1), (1, 2 ** 31 - 1)):
+        assert status(q, None, BF16, 1, k, n, None, None, 0) == UNSUP
+        assert status(d, None, None, 1, k, n, None, BF16, 0) == UNSUP
+    for k, n in ((top, 1), (1, top)):                     # the sizes are taken, the pointers are not
+        assert status(q, None, BF16, 1, k, n, None, None, 0) == INVAL
+        assert status(d, None, None, 1, k, n, None, BF16, 0) == INVAL
+
+
 def test_matmul_int8():
     f = lambda x=P, xs=P, M=8, H=64, N=8, w=P, ws=P, y=P, out=BF16: status(  # noqa: E731
         moe.moe_matmul_int8, x, xs, M, H, N, w, ws, y, out, 0)
