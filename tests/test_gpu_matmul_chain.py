@@ -314,6 +314,115 @@ def test_many_tiles_of_the_weight_gradient(counts, H, N, dtype, out, accumulate)
         assert bool(((dw[e].double() - ref).abs() <= tol).all()), e
 
 
+# ----------------------------------------------------------------------------- gathered rows, every kernel
+#
+# The rows of a group lie anywhere among T tokens, fewer than there are rows; some are padding (-1) or name a token that does
+# not exist. A gathered product is the one of the permuted rows bit for bit: the same kernel and the same order of sums.
+
+GATHERED = [
+    (spread(8, 3000, 1), 24, 520), (spread(8, 3000, 3), 200, 520), (spread(8, 3000, 4), 199, 517),   # many rows, odd sizes
+    ([9000, 3, 0, 700, 1, 0, 129, 5000], 72, 520), ([9000, 3, 0, 700, 1, 0, 129, 5000], 71, 264),    # uneven groups
+    ([900, 1, 7000], 136, 1032), ([900, 1, 7000], 65, 1031), ([30] * 3 + [4000], 64, 1160),
+    (spread(128, 100, 5), 24, 520), (spread(128, 100, 6), 136, 513), (spread(128, 100, 7), 133, 520),
+    (spread(60, 700, 8), 320, 40), (spread(60, 700, 9), 333, 33), ([130, 0, 70, 257], 1032, 72), ([130, 0, 70, 257], 1031, 71),
+    (spread(300, 12, 9), 256, 136), ([5000], 256, 1100), ([33] * 40, 80, 200), ([2] * 90, 264, 104),
+]
+
+
+def draw_gather(g, rows, M, T, K):
+    """row_src for M rows, and where each row lies (padding: -1)."""
+    src = torch.randint(0, T * K, (M,), generator=g, device=DEV, dtype=torch.int32)
+    src[2::11] = -1
+    src[5::13] = torch.randint(T * K, T * K + 1000, (len(src[5::13]),), generator=g, device=DEV, dtype=torch.int32)
+    src[rows:] = 2 ** 31 - 1                       # behind the last group: not looked at
+    at = torch.where((src >= 0) & (src < T * K), src // K, -1).long()
+    return src, at
+
+
+@pytest.mark.parametrize("transposed", [0, 1])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("counts,H,N", GATHERED)
+def test_gathered_rows(counts, H, N, dtype, out, transposed):
+    g = torch.Generator(device=DEV).manual_seed(H + N)
+    d, dt = FMT[dtype]
+    T, K = 301, 3
+    cu, cud, M, E, _, w = draw_rows(g, counts, H, N, dt, transposed)
+    rows = int(cu[-1])
+    src, at = draw_gather(g, rows, M, T, K)
+    x = torch.randn(T, H, generator=g, device=DEV).to(dt)
+    permuted = x[at.clamp(min=0)] * (at >= 0)[:, None].to(dt)
+    y, yp = (torch.full((M, N), 7.0, dtype=FMT[out][1], device=DEV) for _ in range(2))
+    moe.moe_grouped_matmul(x, d, src, T, K, cud, M, E, H, N, w, d, transposed, y, FMT[out][0])
+    moe.moe_grouped_matmul(permuted, d, None, 0, 0, cud, M, E, H, N, w, d, transposed, yp, FMT[out][0])
+    assert torch.equal(y, yp) and bool((y[rows:] == 7.0).all())
+    xd = permuted.double()
+    for e in range(E):
+        a, b = int(cu[e]), int(cu[e + 1])
+        if a == b:
+            continue
+        m = w[e].double().t() if transposed else w[e].double()
+        ref = xd[a:b] @ m
+        tol = H * U * (xd[a:b].abs() @ m.abs())
+        if out == "bf16":
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+        assert bool(((y[a:b].double() - ref).abs() <= tol).all()), e
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,H,N", [(c, h // 16 * 16 + 16, n) for c, h, n in GATHERED])
+def test_gathered_rows_int8(counts, H, N, out):
+    g = torch.Generator(device=DEV).manual_seed(H + N)
+    T, K = 301, 3
+    cu, cud, M, E, _, _ = draw_rows(g, counts, 1, 1, torch.float32, 0)
+    rows = int(cu[-1])
+    src, at = draw_gather(g, rows, M, T, K)
+    code = lambda *s: torch.randint(-128, 128, s, generator=g, device=DEV, dtype=torch.int32).to(torch.int8)  # noqa: E731
+    x, w, w2 = code(T, H), code(E, N, H), code(E, N, H)
+    xs, ws, ws2 = (torch.rand(*s, generator=g, device=DEV) * 0.01 + 0.001 for s in ((T,), (E, N), (E, N)))
+    live = at >= 0
+    xp, xsp = x[at.clamp(min=0)] * live[:, None].to(torch.int8), xs[at.clamp(min=0)] * live.float()
+    d, dt = FMT[out]
+    y, yp = (torch.full((M, N), 7.0, dtype=dt, device=DEV) for _ in range(2))
+    h, hp = (torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    moe.moe_grouped_matmul_int8(x, xs, src, T, K, cud, M, E, H, N, w, ws, y, d)
+    moe.moe_grouped_matmul_int8(xp, xsp, None, 0, 0, cud, M, E, H, N, w, ws, yp, d)
+    moe.moe_ffn_gate_up_int8(x, xs, src, T, K, cud, M, E, H, N, w, w2, ws, ws2, h)
+    moe.moe_ffn_gate_up_int8(xp, xsp, None, 0, 0, cud, M, E, H, N, w, w2, ws, ws2, hp)
+    assert torch.equal(y, yp) and bool((y[rows:] == 7.0).all())
+    assert torch.equal(h, hp) and bool((h[rows:] == 7.0).all())
+    xd = xp.double()
+    for e in range(E):
+        a, b = int(cu[e]), int(cu[e + 1])
+        if a == b:
+            continue
+        s = xsp[a:b, None].double()
+        ref = (xd[a:b] @ w[e].double().t()) * s * ws[e].double()
+        tol = (3 * U + (2.0 ** -8 if out == "bf16" else 0)) * 1.01 * ref.abs()
+        assert bool(((y[a:b].double() - ref).abs() <= tol).all()), e
+        up = (xd[a:b] @ w2[e].double().t()) * s * ws2[e].double()
+        act = ref * torch.sigmoid(ref)
+        hr = act * up
+        tol = (1.1 * 3.01 * U * ref.abs() * up.abs() + act.abs() * 3.01 * U * up.abs() + 16 * U * hr.abs()) * (1 + 2.0 ** -7)
+        assert bool(((h[a:b].double() - hr).abs() <= tol + 2.0 ** -8 * hr.abs() + 2.0 ** -126).all()), e
+    # padding rows are zeros beside columns whose scale is NaN, the others of such a column NaN
+    ws[:, 1::7], ws2[:, 2::7] = float("nan"), float("nan")
+    moe.moe_grouped_matmul_int8(x, xs, src, T, K, cud, M, E, H, N, w, ws, y, d)
+    moe.moe_ffn_gate_up_int8(x, xs, src, T, K, cud, M, E, H, N, w, w2, ws, ws2, h)
+    for t in (y, h):
+        assert bool((t[:rows][~live[:rows]] == 0).all()) and bool(torch.isnan(t[:rows][live[:rows]][:, 1::7]).all())
+    assert bool(torch.isfinite(y[:rows, 0::7]).all()) and bool(torch.isfinite(h[:rows, 0::7]).all())
+
+
+@pytest.mark.parametrize("T,E,K,H,Hp,pad", [(32, 52, 8, 512, 256, 1), (256, 52, 8, 272, 144, 1), (2000, 4, 2, 512, 512, 1),
+                                            (8192, 4, 2, 256, 512, 32)])
+def test_int8_layer_of_batches(T, E, K, H, Hp, pad):
+    """Decode batches over many experts, and prefills whose gathered rows reach the larger tiles."""
+    c = Int8Layer(T, E, K, H, Hp, pad, seed=T)
+    first = c.run().clone()
+    c.check()
+    assert torch.equal(c.run(), first)
+
+
 # ----------------------------------------------------------------------------- past 32 bits
 
 def test_weights_past_4_gib():
