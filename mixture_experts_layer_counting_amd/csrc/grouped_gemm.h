@@ -5,10 +5,10 @@
 //   rows x weights [K][N]     y[r, n]  = sum_k x[r, k] W[k, n]
 //   rows x weights [N][K]     y[r, n]  = sum_k x[r, k] W[n, k]
 //   rows^T x rows             dW[m, n] = sum_r x[r, m] dy[r, n]
-// An operand whose reduction runs along memory (KC) is staged as [rows][128 bytes], the other kind (MC)
-// as [k][columns]. One stage is 128 bytes of reduction per row of a KC operand: 64 bf16, 32 fp32 or 128
-// INT8 elements. In a step kk = 0..3 of a stage, lane l (half g = l / 32) feeds the matrix cores the 16 bytes of chunk 2 kk + g
-// of its row or column l % 32:
+// An operand whose reduction runs along memory (KC) is staged as [rows][128 bytes], the other kind (MC) as
+// [k][columns]. One stage is 128 bytes of reduction per row of a KC operand: 64 bf16, 32 fp32 or 128 INT8
+// elements. In a step kk = 0..3 of a stage, lane l (half g = l / 32) feeds the matrix cores the 16 bytes of
+// chunk 2 kk + g of its row or column l % 32:
 //   bf16  v_mfma_f32_32x32x16_bf16, eight elements a lane: one instruction
 //   INT8  v_mfma_i32_32x32x32_i8, sixteen: one instruction
 //   fp32  v_mfma_f32_32x32x2_f32, one element a lane: four instructions, element j of each chunk
@@ -187,7 +187,7 @@ __device__ __forceinline__ i32x4_t first_of_chunk(i32x4_t v, int n) {
 
 // ---- epilogue --------------------------------------------------------------------------
 
-// Eight values of a row: v[0..3] at columns c .. c + 3 and v[4..7] at c + 8 .. c + 11, where c = c0 + 4 (lane / 32);
+// Eight values of a row: v[0..3] at columns c .. c + 3 and v[4..7] at c + 8 .. c + 11, c = c0 + 4 (lane / 32);
 // the wave's row block covers columns c0 .. c0 + 15. `vec`: rows are whole 16-byte words of the output.
 template <bool OUT_F32>
 __device__ __forceinline__ void store_run(void* C, size_t row, int N, int c0, int lane, bool ok, bool vec,
@@ -232,9 +232,10 @@ __device__ __forceinline__ bool whole_words(const void* C, int N) {
 
 // ---- bf16 rows that are not whole 16-byte words --------------------------------------------
 //
-// Tiles of T x T by four waves; a thread loads its chunks of a stage into
-// registers PD stages ahead and writes them to one of two LDS buffers. A chunk that reaches past its row reads the next row's elements,
-// which count for columns that are not stored or are cut off in the last stage of the reduction. TN: rows^T x rows.
+// Tiles of T x T by four waves; a thread loads its chunks of a stage into registers PD stages ahead and
+// writes them to one of two LDS buffers. A chunk that reaches past its row reads the next row's elements,
+// which count for columns that are not stored or are cut off in the last stage of the reduction.
+// TN: rows^T x rows.
 constexpr int GA_THREADS = 256;
 
 template <bool AKC, bool BKC, bool OUT_F32, int T, int PD>

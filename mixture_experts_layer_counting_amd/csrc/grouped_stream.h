@@ -1,16 +1,18 @@
 // Grouped products with few rows and few columns: the weights are read once and hardly reused, so what counts
-// is to have many of their bytes in flight. A wave takes a few columns and a slice of the reduction and streams the
-// weights past up to 16 rows straight into registers, with the weights as the first operand of the 16 x 16 matrix
-// instructions (lane l: column l % 16, quarter G = l / 16 of the instruction's k) and the rows as the second.
+// is to have many of their bytes in flight. A wave takes a few columns and a slice of the reduction and
+// streams the weights past up to 16 rows straight into registers, with the weights as the first operand of
+// the 16 x 16 matrix instructions (lane l: column l % 16, quarter G = l / 16 of the instruction's k) and the
+// rows as the second.
 //   weights [N][K]  16 columns a wave. In a step a lane takes the 64 bytes at 64 G of its column's next 256: two whole
 //                   lines per column and step. Which k an instruction multiplies is free as long as the rows agree.
 //   weights [K][N]  64 columns a wave, 32 k a step. A lane takes four neighbouring columns of the eight k rows
 //                   8 G + j; instruction i multiplies the columns 4 (l % 16) + i. bf16 pairs of rows are brought
 //                   together by byte permutes, fp32 needs none.
-// What bounds it is the weights' HBM stream: one token of 8 experts, 7168 x 2048, weights not cached: bf16 44 us (235 MB, 5.4 TB/s), INT8
-// gate/up 50 (235 MB, 4.7 TB/s); one row of a dense INT8 7168 x 2048, 14.7 MB, 6-7 us: the launch and one trip to memory.
-// The next step's loads are out before this one's products. A block of eight waves splits the reduction `ks` ways
-// and adds the slices in their order through LDS, so the result does not depend on timing. An expert
+// What bounds it is the weights' HBM stream: one token of 8 experts, 7168 x 2048, weights not cached: bf16 44
+// us (235 MB, 5.3 TB/s; a plain read of 4 GiB reaches 5.95), INT8 gate/up 50 (235 MB, 4.7 TB/s); one row of a
+// dense INT8 7168 x 2048, 14.7 MB, 6-7 us: the launch and one trip to memory.
+// The next step's loads are out before this one's products. A block of eight waves splits the reduction `ks`
+// ways and adds the slices in their order through LDS, so the result does not depend on timing. An expert
 // with more rows gets a block per 16 of them.
 #pragma once
 
@@ -60,7 +62,8 @@ __global__ __launch_bounds__(GS_THREADS) void gg_stream_kernel(GgArgs a, int ks)
   const int groups = WM / ks;                   // column groups of a block
   const int BN = groups * WC;
   const int ncb = (N + BN - 1) / BN;
-  // Eight neighbours on one XCD (they share lines at their borders, and a heavy expert's panels), the eights round-robin.
+  // Eight neighbours on one XCD (they share lines at their borders, and a heavy expert's panels), the eights
+  // round-robin.
   const int whole = gridDim.x & ~63;
   const int b = blockIdx.x;
   const int idx = b < whole ? (b & ~63) + (b & 7) * 8 + ((b >> 3) & 7) : b;
@@ -235,10 +238,11 @@ moe_status_t launch_gg_stream(const GgArgs& a, hipStream_t s) {
   const int64_t slots = a.M < a.E ? a.M : a.E;  // at most so many experts have rows
   // n experts with R rows make at most n + (R - n) / 16 chunks; blocks past the last one have none
   const int64_t chunks = slots + (a.M - slots) / 16;
-  // Slices of the reduction: as many as leave 8 waves a CU (fp32, whose products take longer: 16). Measured, us, by 8 / 4 / 2 / 1
-  // slices, weights not in a cache (gated: 4 / 2 / 1): INT8 1 x 7168 x 2048 (128 waves unsplit) 7 / 11 / 18 / 33; gate/up, 8 experts
-  // 7168 x 2048 (2048) 57 / 58 / 50; bf16 [K][N], 8 experts 7168 x 2048 (256) 44 / 68 / 125 / 243. In a cache: INT8, 8 experts
-  // 7168 x 2048 (1024) 24.5 / 24.2 / 23.9 / 39, 2048 x 7168 (3584) 37 / 31 / 26 / 25; fp32, 64 experts 2048 x 1024 (1024) 101 / 98 / - / 153.
+  // Slices of the reduction: as many as leave 8 waves a CU (fp32, whose products take longer: 16). Measured,
+  // us, by 8 / 4 / 2 / 1 slices, weights not in a cache (gated: 4 / 2 / 1): INT8 1 x 7168 x 2048 (128 waves
+  // unsplit) 7 / 11 / 18 / 33; gate/up, 8 experts 7168 x 2048 (2048) 57 / 58 / 50; bf16 [K][N], 8 experts
+  // 7168 x 2048 (256) 44 / 68 / 125 / 243. In a cache: INT8, 8 experts 7168 x 2048 (1024) 24.5 / 24.2 / 23.9
+  // / 39, 2048 x 7168 (3584) 37 / 31 / 26 / 25; fp32, 64 experts 2048 x 1024 (1024) 101 / 98 / - / 153.
   // (counted for evenly filled groups)
   const int64_t waves = slots * (((a.M + slots - 1) / slots + 15) / 16) * ((a.N + WC - 1) / WC) * (GATED ? 2 : 1);
   int ks = WM;

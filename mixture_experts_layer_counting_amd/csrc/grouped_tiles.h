@@ -1,19 +1,25 @@
-// Tiles of the grouped products for rows of whole 16-byte words, or in fp32 of any length: both operands go from memory to LDS directly, two stages in
-// turn, and within a wave the loads of the next stage and the fragment reads of the next step are spread between
-// the products of this one, across the stage barrier too.
+// Tiles of the grouped products for rows of whole 16-byte words, or in fp32 of any length: both operands go
+// from memory to LDS directly, two stages in turn, and within a wave the loads of the next stage and the
+// fragment reads of the next step are spread between the products of this one, across the stage barrier too.
 //
-// A block of WM x WN waves, each with MT x NT blocks of 32 x 32. A wave's row blocks lie WM * 32 rows apart, so that
-// the padded rows of a group's last tile fall on all waves alike; a wave skips the blocks that lie wholly past the rows.
-// The next tile's first stage is loaded under the last stage of this one and waited for before the stores go out, so that its
-// first products need a barrier only; the stores have until its second stage.
+// A block of WM x WN waves, each with MT x NT blocks of 32 x 32. A wave's row blocks lie WM * 32 rows apart,
+// so that the padded rows of a group's last tile fall on all waves alike; a wave skips the blocks that lie
+// wholly past the rows.
+// The next tile's first stage is loaded under the last stage of this one and waited for before the stores go
+// out, so that its first products need a barrier only; the stores have until its second stage.
 //
-// What bounds it, 256 x 256 tiles. 8192^3: INT8 2.50 POP/s (a library's product 1.96), bf16 1.33 PFLOP/s (1.19 with the weights [K][N], 1.50
-// with [N][K]): the matrix cores are busy for 69 and 75 % of the cycles, at 1.7 GHz: the power limit. 65536 rows over 52 experts, us:
-// 7168 x 2048 INT8 867 (2.2 POP/s), bf16 1650-1680 (1.16 PFLOP/s); 2048 x 7168 INT8 1030 (1.9), bf16 1730; gate/up INT8 1700.
-// With 384 rows per expert (64 experts, 2048 x 1024) weights, rows and results, 419 MB, bound it: bf16 122 us (3.4 TB/s), INT8 62.
-// dW: 65536 rows over 52 experts, 2048 x 7168 2.0 ms; without its 3 GB of stores 1.55: the tile's 256 KB leave its CU at the rate at
-// which all CUs together fill the memory (5.5 TB/s), and its waves' loads wait behind them (one counter counts both, in order).
-// Two blocks of 256 x 128 with half the stage, one computing while the other stores: 2.27; blocks started out of phase: no change.
+// What bounds it, 256 x 256 tiles. 8192^3: INT8 2.46 POP/s (a library's product 2.02), bf16 1.33-1.34 PFLOP/s
+// in both weight orders (a library's 1.19 with the weights [K][N], 1.52 with [N][K]): the matrix cores are
+// busy for 68 and 72 % of the cycles, at 1.75 GHz: the power limit. 65536 rows over 52 experts, us:
+// 7168 x 2048 INT8 867 (2.2 POP/s), bf16 1650-1680 (1.16 PFLOP/s); 2048 x 7168 INT8 1030 (1.9), bf16 1730;
+// gate/up INT8 1700.
+// 384 rows per expert (64 experts, 2048 x 1024, operands read again): bf16 122 us (419 MB, 3.4 TB/s), INT8 62.
+// They make two tiles of 192 rows, of whose four row-waves two have one block instead of two: a quarter of
+// the matrix cores' time is empty.
+// dW: 65536 rows over 52 experts, 2048 x 7168 2.0 ms; without its 3 GB of stores 1.55: the tile's 256 KB
+// leave its CU at the rate at which all CUs together fill the memory (5.5 TB/s), and its waves' loads wait
+// behind them (one counter counts both, in order). Two blocks of 256 x 128 with half the stage, one computing
+// while the other stores: 2.27; blocks started out of phase: no change.
 #pragma once
 
 #include "grouped_gemm.h"
@@ -23,14 +29,16 @@ namespace moe {
 constexpr int GT_PANEL = 8;
 constexpr int GT_OUT = (int)0x80000000u;  // an offset past every range: loads zeros
 
-// A 32 x 32 block of fp32 whose lane l holds row l % 32 and, in v[4 j + c], column 8 j + 4 (l / 32) + c, to rows of whole 16-byte words, turned
-// through 4.5 KB of LDS that no other wave uses: eight lanes then hold the 128 bytes of a row. `rows`: how many of the 32 there
-// are; p: the first one's first column; `left`: columns from there on. All lanes must be active.
-// A store then writes whole lines, 1 KB in all: dW, 64 experts of 384 rows, 2048 x 1024 188 -> 179 us beside a column per lane and 4 bytes
-// (64 rows over 64 experts, nothing but stores, 97 -> 102).
-// PAST: the stores ask the caches not to keep them. For weight gradients, which outgrow the caches and are read much later, where
-// rows are whole lines (us, kept / past, operands read again): 64 experts 2048 x 1024 179 / 152, 8 of 4096 x 4096 307 / 275, 52 of 2048 x
-// 7168 2059 / 2019; rows that share lines the other way, 2048 x 1000 231 / 257.
+// A 32 x 32 block of fp32 whose lane l holds row l % 32 and, in v[4 j + c], column 8 j + 4 (l / 32) + c, to
+// rows of whole 16-byte words, turned through 4.5 KB of LDS that no other wave uses: eight lanes then hold
+// the 128 bytes of a row. `rows`: how many of the 32 there are; p: the first one's first column; `left`:
+// columns from there on. All lanes must be active.
+// A store then writes whole lines, 1 KB in all: dW, 64 experts of 384 rows, 2048 x 1024 188 -> 179 us beside
+// a column per lane and 4 bytes (64 rows over 64 experts, nothing but stores, 97 -> 102).
+// PAST: the stores ask the caches not to keep them. For weight gradients, which outgrow the caches and are
+// read much later, where rows are whole lines (us, kept / past, operands read again): 64 experts 2048 x 1024
+// 179 / 152, 8 of 4096 x 4096 307 / 275, 52 of 2048 x 7168 2059 / 2019; rows that share lines the other way,
+// 2048 x 1000 231 / 257.
 constexpr int GT_TURN = 32 * 144;  // rows of 128 bytes, 16 apart: neighbours begin on other banks
 template <bool PAST>
 __device__ __forceinline__ void store_turned(unsigned char* turn, float* p, int N, int rows, int left, int lane, bool add,
@@ -84,7 +92,8 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   constexpr int BN = GATED ? CF::BN / 2 : CF::BN;  // columns per matrix
   constexpr int SCN = BN < 64 ? 64 : BN;           // and their places among the scales
   constexpr int NS = CF::NS;
-  // fp32 gradients whose rows are not whole words leave with a column per lane, 128 neighbouring bytes of two rows a store
+  // fp32 gradients whose rows are not whole words leave with a column per lane, 128 neighbouring bytes of two
+  // rows a store
   constexpr bool COL_LANES = TN && CF::DW;
   static_assert(W * GT_TURN <= CF::STAGE, "a wave's share of a stage");
   using SA = Staged<EL, AKC, BM>;
@@ -103,11 +112,12 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   if constexpr (TN) total = a.E * mtn * ntn;
   else total = group_prefix<CF::THREADS>(a.cu, a.M, a.E, [&](int rows) { return (rows + BM - 1) / BM * ntn; }, tstart, wsum);
   const int G = gridDim.x;
-  // Round by round, the blocks of an XCD take neighbouring tiles. The last round, which may have fewer tiles than blocks, gives each
-  // XCD an eighth of them; where at most one whole round went before and tiles are left for half of the blocks or fewer,
-  // they are cut along the rows into two or four parts, one a block. Dense INT8, 7168 reduction, us: 6000 x 2048 (192 tiles of
-  // 256 x 256) 99 -> 84, 8000 x 2304 (288) 162 -> 142; bf16, 8 experts of 512 rows, 2048 x 1024 35 -> 27. Cut after
-  // more rounds it costs more than it gives, as the clock rises while few CUs work: 65536 rows over 52 experts (2080) 867 -> 886.
+  // Round by round, the blocks of an XCD take neighbouring tiles. The last round, which may have fewer tiles
+  // than blocks, gives each XCD an eighth of them; where at most one whole round went before and tiles are
+  // left for half of the blocks or fewer, they are cut along the rows into two or four parts, one a block.
+  // Dense INT8, 7168 reduction, us: 6000 x 2048 (192 tiles of 256 x 256) 99 -> 84, 8000 x 2304 (288) 162 ->
+  // 142; bf16, 8 experts of 512 rows, 2048 x 1024 35 -> 27. Cut after more rounds it costs more than it
+  // gives, as the clock rises while few CUs work: 65536 rows over 52 experts (2080) 867 -> 886.
   const int slot = xcd_slot(blockIdx.x, G);
   const int whole = total / G * G, rest_tiles = total - whole;
   constexpr int MOST = TN ? 1 : BM / 64;
@@ -121,7 +131,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   const uint32_t lds0 = lds_addr(smem);
   const int pitch = Kd * ES, npitch = N * ES;  // bytes of a KC row, of an MC row of B (and pitch: of A, TN)
 
-  // Wave load j = wave + W i fills chunks 64 j .. 64 j + 63 of an operand's stage (DW: dwords 64 j .. 64 j + 63).
+  // Wave load j = wave + W i fills chunks 64 j to 64 j + 63 of an operand's stage (DW: those dwords).
   auto chunk_of = [&](int i) __attribute__((always_inline)) {
     return CF::DW ? (wave + W * i) * 16 + (lane >> 2) : (wave + W * i) * 64 + lane;
   };
@@ -176,7 +186,8 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
     } else {
       const int lt = t - tstart[d.e];
       const int mte = (rows_e + BM - 1) / BM;
-      // eight row tiles under one column tile, then the next column tile: the blocks of an XCD share rows and columns
+      // eight row tiles under one column tile, then the next column tile: the blocks of an XCD share rows and
+      // columns
       const int panel = lt / (GT_PANEL * ntn), in_panel = lt - panel * GT_PANEL * ntn;
       const int deep = min(GT_PANEL, mte - panel * GT_PANEL);
       ntile = in_panel / deep;
@@ -372,8 +383,8 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
         step(f1, f0, st, integral_constant<int, 2>{}, std::false_type{}, cur, 0, false);
         step(f0, f1, st, integral_constant<int, 3>{}, std::false_type{}, cur, 0, false);
       };
-      // A stage: it has landed for every wave (at most `younger` loads are outstanding), and every wave has read all
-      // it needs of the buffer before it, into which stage `kl` of tile d goes.
+      // A stage: it has landed for every wave (at most `younger` loads are outstanding), and every wave has
+      // read all it needs of the buffer before it, into which stage `kl` of tile d goes.
       auto stage = [&](const Tile& d, int kl, bool load, int younger) __attribute__((always_inline)) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_vm_dyn<(NS - 2) * PIECES>(younger);
@@ -403,7 +414,7 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
       }
       if constexpr (MTV > 0) step(f1, f0, smem, integral_constant<int, -1>{}, std::false_type{}, cur, 0, false);
     };
-    // (NS = 2: every wave waited for its loads of this tile's first stage); the reads of the last tile's are done
+    // (NS = 2: every wave waited for its loads of this tile's first stage); the last tile's reads are done
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if constexpr (NS == 2) {
       if (cur.nk > 1) load_all(cur, 1, buf ^ 1);
@@ -526,10 +537,10 @@ __global__ __launch_bounds__(CF::THREADS, 2) void gg_tile_kernel(GgArgs a) {
   }
 }
 
-// The forms of the kernel: 256 x 256 by eight waves; 128 x 128 by four, two blocks a CU; 128 x 64 by four with four
-// stages in LDS, for products whose tiles are so few that the loads' latency counts.
-// (Large with two waves down and four across, which halves the rows a wave may skip, took 1.5-2.5 % longer on every
-// shape: INT8, 65536 rows over 52 experts, 7168 x 2048 883 us beside 863.)
+// The forms of the kernel: 256 x 256 by eight waves; 128 x 128 by four, two blocks a CU; 128 x 64 by four
+// with four stages in LDS, for products whose tiles are so few that the loads' latency counts.
+// (Large with two waves down and four across, which halves the rows a wave may skip, took 1.5-2.5 % longer on
+// every shape: INT8, 65536 rows over 52 experts, 7168 x 2048 883 us beside 863.)
 template <class EL>
 using GtLarge = GtCfg<EL, 4, 2, 2, 4>;
 template <class EL>
@@ -542,12 +553,15 @@ using GtThinDw = GtCfg<ElF32, 4, 1, 1, 2, 4, true>;
 
 enum GgForm { GG_STREAM, GG_THIN, GG_SMALL, GG_LARGE };
 
-// Which kernel takes a product whose rows are whole 16-byte words, from the number of 128 x 64 tiles (`thin`; of both matrices
-// where gated) and the rows per group. Measured on 256 CUs, us, stream / thin / small / large, rows per group in brackets:
+// Which kernel takes a product whose rows are whole 16-byte words, from the number of 128 x 64 tiles (`thin`;
+// of both matrices where gated) and the rows per group. Measured on 256 CUs, us, stream / thin / small /
+// large, rows per group in brackets:
 //   INT8, dense 7168 x 2048 (32 thin tiles): [1] 7.5 / 23 / 35 / 50  [16] 10 / 23 / 36 / 50  [64] 16 / 23 / 38 / 54
-//                                           [128] 30 / 25 / 43 / 54  [2048, 512 tiles] - / 50 / 58 / 99  [4096] - / 130 / 62 / 103
-//   INT8, 8 experts 7168 x 2048 (256): [1] 22 / 24 / 49 / 57  [8] 25 / 24 / 49 / 57  [16] 32 / 25 / 50 / 57  [128] 200 / 27 / 62 / 67
-//   bf16 [N][K], the same: [1] 39 / 42 / 92 / 104  [8] 44 / 42 / 92 / 105  [16] 58 / 43 / 92 / 105; 16 experts 1024 x 512 (128): [16] 7 / 9 / 17 / 19
+//     [128] 30 / 25 / 43 / 54  [2048, 512 tiles] - / 50 / 58 / 99  [4096] - / 130 / 62 / 103
+//   INT8, 8 experts 7168 x 2048 (256): [1] 22 / 24 / 49 / 57  [8] 25 / 24 / 49 / 57  [16] 32 / 25 / 50 / 57
+//     [128] 200 / 27 / 62 / 67
+//   bf16 [N][K], the same: [1] 39 / 42 / 92 / 104  [8] 44 / 42 / 92 / 105  [16] 58 / 43 / 92 / 105
+//   bf16 [N][K], 16 experts 1024 x 512 (128): [16] 7 / 9 / 17 / 19
 //   INT8 gate/up, the same (512): [1] 40 / 49 / 63 / 67  [8] 47 / 49 / 63 / 67  [16] 57 / 49 / 64 / 67
 //   INT8, 8 experts 2048 x 7168 (896): [1] 25 / 34 / 22 / 24  [16] 35 / 33 / 23 / 25
 //   bf16 [K][N], 8 experts 7168 x 2048 (256): [1] 37 / 44 / 93 / 103  [16] 39 / 44 / 94 / 102  [128] 158 / 48 / 110 / 115

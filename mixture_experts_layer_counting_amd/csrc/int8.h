@@ -20,10 +20,11 @@ __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
 }
 
 // Codes of n values with their scales s and inv = fl32(1 / s), as the low bytes of code[].
-// x inv, rounded once to an integer by the addition of 1.5 * 2^23 (whose low byte is then the code), is off from x / s by less than
-// 2^-16 (|x / s| <= 127.01, inv by 2^-24 of it): only a quotient within 2^-13 of a half step can round the wrong way.
-// There the border b = n + 1/2 is compared with x itself: b s has at most 32 significant bits and fma rounds once, so the sign
-// of x - b s is exact. `bad`: some inv is 0, a column with a NaN or an infinity, whose codes are 0.
+// x inv, rounded once to an integer by the addition of 1.5 * 2^23 (whose low byte is then the code), is off
+// from x / s by less than 2^-16 (|x / s| <= 127.01, inv by 2^-24 of it): only a quotient within 2^-13 of a
+// half step can round the wrong way. There the border b = n + 1/2 is compared with x itself: b s has at most 32 significant
+// bits and fma rounds once, so the sign of x - b s is exact. `bad`: some inv is 0, a column with a NaN or an
+// infinity, whose codes are 0.
 template <int N, int NS>
 __device__ __forceinline__ void int8_codes(const float (&x)[N], const float (&s)[NS], const float (&inv)[NS], bool bad,
                                            uint32_t (&code)[N]) {

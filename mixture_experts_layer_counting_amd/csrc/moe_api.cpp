@@ -539,8 +539,9 @@ moe_status_t moe_dequantize_int8_weights(const int8_t* q, const float* sf, int32
   return launch_dequantize_int8_weights(q, sf, E, K, N, out, out_dtype, stream);
 }
 
-// Sizes that the grouped products share: tiles are counted in 31 bits (at least 64 rows and columns each), and
-// offsets into 256 rows, or into 128 reduction steps of columns, are 32-bit.
+// Sizes that the grouped products share: tiles are counted in 31 bits (64 x 64 results at least; a gated product's
+// 128 x 32 are taken where they are few or N <= 32), and offsets into 256 rows, or into 64 reduction steps of
+// columns, are 32-bit.
 static moe_status_t check_grouped(int64_t M, int64_t E, int64_t H, int64_t N) {
   if (M < 0 || E < 1 || H < 1 || N < 1) return MOE_EINVAL;
   if (M > 1 << 30 || E > 1024 || H > 1 << 20 || N > 1 << 20) return MOE_EUNSUPPORTED;

@@ -7,11 +7,15 @@
 //  weights:  w [E, K, N] (reduction first) -> q [E, N, K], sf [E, N]. The maximum of a column needs all
 //            of K before the first code, so the values are read twice; codes are turned through LDS
 //            and written in runs along k.
-// All are bound by HBM (a large copy reaches 4.8 TB/s here): rows 8191 x 7168 bf16 34 us, 5.2 TB/s, and back 26.5; 65536 x 2048
-// 69; weights 64 x 2048 x 1024 fp32 212-220 us, 5.6 TB/s over both reads, and back to bf16 90; 52 x 7168 x 2048 bf16 790-805, and
-// back 447-467. The second read of the weights costs a third to a half of a call that is made once per weight: values that stay in registers
-// between the passes would need a whole column's reduction per block. Any C, K and N: rows may start at any element, whole 16-byte words are
-// loaded where they lie inside the row and single elements at its end.
+// All are bound by HBM (a large copy reaches 4.8 TB/s here): rows 8191 x 7168 bf16, operands not cached 41 us
+// (4.25 TB/s), read and written again 35, and back 33 and 27; 65536 x 2048 70 either way (5.75 TB/s);
+// operands read and written again: weights 64 x 2048 x 1024 fp32 212-220 us, 5.6 TB/s over both reads, and
+// back to bf16 90; 52 x 7168 x 2048 bf16 790-805, and back 447-467. The second read of the weights costs a
+// third to a half of a call that is made once per weight: values that stay in registers between the passes
+// need a column's whole reduction in one block, which holds for K up to some 2048 in fp32 (32 columns: 256 KB
+// of a CU's 512) and was not tried.
+// Any C, K and N: rows may start at any element, whole 16-byte words are loaded where they lie inside the row
+// and single elements at its end.
 #include "int8.h"
 #include "tile_sched.h"
 
@@ -36,8 +40,8 @@ __device__ __forceinline__ void load8(const XT* p, float (&v)[8]) {
   }
 }
 
-// The first n (at most eight, or none) of them; the others zero. A loop over several takes the whole ones without a branch in
-// between, or each would wait for the one before.
+// The first n (at most eight, or none) of them; the others zero. A loop over several takes the whole ones
+// without a branch in between, or each would wait for the one before.
 template <typename XT>
 __device__ __forceinline__ void load8(const XT* p, int n, float (&v)[8]) {
   if (n >= 8) {
@@ -174,19 +178,21 @@ __global__ __launch_bounds__(256) void dequant_rows_i8_kernel(const int8_t* __re
 }
 
 // ---- weights -----------------------------------------------------------------------------
-// Slabs of 64 columns: eight lanes side by side take eight columns each. The threads of a block along k take four neighbouring
-// rows each, so that four codes of a column make one dword of the turned tile [column][k] in LDS. Its rows are 65 dwords long:
-// the dwords that a wave writes (eight columns apart, eight along k) fall on different banks. (Slabs of 128 columns of
-// bf16, 256 bytes of a row, took longer: 52 x 7168 x 2048 930 us against 809, and back 582 against 446.)
+// Slabs of 64 columns: eight lanes side by side take eight columns each. The threads of a block along k take
+// four neighbouring rows each, so that four codes of a column make one dword of the turned tile [column][k]
+// in LDS. Its rows are 65 dwords long: the dwords that a wave writes (eight columns apart, eight along k)
+// fall on different banks. (Slabs of 128 columns of bf16, 256 bytes of a row, took longer: 52 x 7168 x 2048
+// 930 us against 809, and back 582 against 446.)
 constexpr int QW_THREADS = 512;
 constexpr int QW_COLS = 64, QW_K = 256;
 constexpr int QW_LD = QW_K / 4 + 1;
 
-// First of the eight columns of a lane whose own begin at n: the last eight where fewer are left (shared with its neighbour,
-// computed twice, alike).
+// First of the eight columns of a lane whose own begin at n: the last eight where fewer are left (shared with
+// its neighbour, computed twice, alike).
 __device__ __forceinline__ int first_column(int n, int N) { return N >= 8 ? min(n, N - 8) : n; }
 
-// Block b of G: neighbours on one XCD, so that the lines that two tiles or slabs share (rows that do not end on whole lines) meet in one L2.
+// Block b of G: neighbours on one XCD, so that the lines that two tiles or slabs share (rows that do not end
+// on whole lines) meet in one L2.
 __device__ __forceinline__ int64_t near_block(int b, int G) {
   const int even = G & ~7;
   return b < even ? xcd_slot(b, even) : b;
@@ -194,8 +200,8 @@ __device__ __forceinline__ int64_t near_block(int b, int G) {
 
 typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
 
-// Largest magnitudes of the n columns from p on (at most eight count; none: n = 0) over the K rows of w, joined over the
-// block: best[..][first + i].
+// Largest magnitudes of the n columns from p on (at most eight count; none: n = 0) over the K rows of w,
+// joined over the block: best[..][first + i].
 // Eight rows are loaded before the first is looked at: the bytes in flight bound this pass.
 template <int WAVES, typename XT>
 __device__ __forceinline__ void column_max(const XT* p, int n, int first, int K, int N, uint32_t (&best)[WAVES][QW_COLS]) {
@@ -268,7 +274,8 @@ __global__ __launch_bounds__(1024) void weight_scales_i8_kernel(const XT* __rest
   }
 }
 
-// Codes, a turned tile at a time, last tiles first: what the scales' pass read last is still in the last-level cache.
+// Codes, a turned tile at a time, last tiles first: what the scales' pass read last is still in the
+// last-level cache.
 template <typename XT>
 __global__ __launch_bounds__(QW_THREADS) void quant_weights_i8_kernel(const XT* __restrict__ w, int K, int N, int ncb,
                                                                       int ny, int64_t tiles,
@@ -386,7 +393,7 @@ unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < MAX_GRID ? blocks 
 
 template <typename XT>
 moe_status_t quantize_rows(const XT* x, int R, int C, int8_t* q, float* sf, hipStream_t s) {
-  // a wave per row holds up to 2048 values (65536 rows of 2048 took 118 us with a block each), a block up to 8192
+  // a wave per row holds up to 2048 values (65536 rows of 2048: 118 us with a block each), a block 8192
   if (C <= 512)
     quant_rows_i8_kernel<XT, 64, 1><<<grid_of(((int64_t)R + 3) / 4), 256, 0, s>>>(x, R, C, q, sf);
   else if (C <= 1024)
