@@ -288,3 +288,36 @@ def test_grouped_ffn(counts, H, Hp):
     got = y.double().cpu().numpy()
     assert (np.abs(got[:c.rows] - ref) <= (3 * U + 2.0 ** -8) * 1.01 * np.abs(ref)).all()
     assert (got[c.rows:] == 7.0).all() and bool((yg == 7.0).all()) and bool((wg == 0x55).all())
+
+
+@pytest.mark.parametrize("rows", [9, 400])
+def test_padding_rows_of_the_ffn(rows):
+    """Their h is zeros whatever the gate and up weights hold, and goes through the down product as a row of zeros: zeros, but
+    NaN in a column of NaN scale. Rows beside them are not touched by it."""
+    H, Hp, E, T = 64, 48, 2, 20
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    code = lambda *s: torch.randint(-127, 128, s, generator=g, device=DEV, dtype=torch.int32).to(torch.int8)  # noqa: E731
+    x, wg, wu, wd = code(T, H), code(E, Hp, H), code(E, Hp, H), code(E, H, Hp)
+    xs, sg, su, sd = (torch.full(s, 0.01, device=DEV) for s in ((T,), (E, Hp), (E, Hp), (E, H)))
+    src = torch.randint(0, T, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    src[1::4] = -1
+    pad = (src < 0).cpu()
+    cu = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device=DEV)
+    n = moe.moe_grouped_ffn_int8_workspace_bytes(rows, Hp)
+    ws, y = torch.empty(n, dtype=torch.uint8, device=DEV), torch.empty(rows, H, dtype=torch.bfloat16, device=DEV)
+
+    def ffn():
+        moe.moe_grouped_ffn_int8(x, xs, src, T, 1, cu, rows, E, H, Hp, wg, wu, wd, sg, su, sd, y, ws, n)
+        torch.cuda.synchronize()
+        return y.float().cpu()
+
+    first = ffn()
+    assert bool((first[pad] == 0).all()) and bool(torch.isfinite(first).all())
+    sd[:, 5] = float("nan")
+    out = ffn()
+    assert bool(torch.isnan(out[:, 5]).all())
+    keep = [c for c in range(H) if c != 5]
+    assert torch.equal(out[:, keep], first[:, keep])
+    sg[:, 3] = float("nan")                                # h of the other rows is NaN there, and their y everywhere
+    out = ffn()
+    assert bool((out[pad][:, keep] == 0).all()) and bool(torch.isnan(out[~pad]).all())
