@@ -562,8 +562,10 @@ MOE_API size_t moe_grouped_ffn_int8_workspace_bytes(int32_t M, int32_t Hp);
 
 /* The expert FFN in INT8: moe_ffn_gate_up_int8, h quantised per row (moe_quantize_int8), and the down product
  * y_rows[r] = h[r] . Wd[e] (moe_grouped_matmul_int8; w_down [E, H, Hp], sf_down [E, H]), y_rows [M, H] bf16. h, its
- * codes and scales live in `ws` (16-byte aligned); calls that share a workspace must be ordered. Needs the limits
- * of both products (H % 16 == 0 and Hp % 16 == 0 among them). Three kernel launches. */
+ * codes and scales live in `ws` (16-byte aligned); calls that share a workspace must be ordered. The h of a padding
+ * row is zeros and goes through the down product like any row of zeros: its y is zeros, but NaN in a column whose
+ * scale sf_down is NaN. Needs the limits of both products (H % 16 == 0 and Hp % 16 == 0 among them). Three kernel
+ * launches. */
 MOE_API moe_status_t moe_grouped_ffn_int8(const int8_t* x_q, const float* x_sf, const int32_t* row_src, int32_t T,
                                           int32_t K, const int32_t* cu_seqlens, int32_t M, int32_t E, int32_t H,
                                           int32_t Hp, const int8_t* w_gate, const int8_t* w_up, const int8_t* w_down,
